@@ -86,8 +86,15 @@ typedef enum pkv_status {
 } pkv_status;
 
 /* Element types.  PKV_FP8_E4M3 is a cache type only (one byte per element,
- * one float scale per cache tensor; see pkv_kv_append_fp8). */
-typedef enum pkv_dtype { PKV_F32 = 0, PKV_BF16 = 1, PKV_F16 = 2, PKV_FP8_E4M3 = 3 } pkv_dtype;
+ * one float scale per cache tensor; see pkv_kv_append_fp8), and so is
+ * PKV_FP4_E2M1 (4-bit codes with a scale for 16 of them; pkv_kv_append_fp4). */
+typedef enum pkv_dtype {
+  PKV_F32 = 0,
+  PKV_BF16 = 1,
+  PKV_F16 = 2,
+  PKV_FP8_E4M3 = 3,
+  PKV_FP4_E2M1 = 4
+} pkv_dtype;
 
 /* Codes the kernels record in the optional device error word. */
 enum {
@@ -95,7 +102,8 @@ enum {
   PKV_DEVERR_SLOT = 1,        /* kv_append: slot >= num_blocks * block_size */
   PKV_DEVERR_BLOCK_ID = 2,    /* block_table entry outside [0, num_blocks) */
   PKV_DEVERR_CONTEXT_LEN = 3, /* context_lens[b] > max_context_len or > table */
-  PKV_DEVERR_TIMEOUT = 4      /* a shared-memory copy did not arrive in time */
+  PKV_DEVERR_TIMEOUT = 4,     /* a shared-memory copy did not arrive in time */
+  PKV_DEVERR_PATH = 5         /* pkv_commit_rows: a path that is not increasing tree nodes */
 };
 
 /* Kernel families. */
@@ -428,6 +436,104 @@ PKV_API pkv_status pkv_paged_attention_fp8(
     int block_size, int64_t num_blocks, float scale, pkv_dtype q_dtype,
     float k_scale, float v_scale, void *workspace, size_t workspace_bytes,
     const pkv_options *options, int32_t *error_word, pkv_stream_t stream);
+
+/*
+ * Block-scaled 4-bit KV cache.  A value is  code * block scale * tensor scale:
+ * the code is E2M1 (a sign and 0, 0.5, 1, 1.5, 2, 3, 4 or 6), the block scale
+ * E4M3, one for every 16 consecutive head dims of a row, and the tensor scale
+ * one float per cache tensor; 4.5 bits a value.  A cache is
+ * [num_blocks, num_kv_heads, 9 * head_dim] bytes: the tile of one (block, KV
+ * head) is contiguous and holds the codes of its 16 rows, two to a byte (even
+ * dim in the low nibble), then their scales,
+ *   keys    codes [head_dim / P][16 rows][P / 2], P = min(head_dim, 128);
+ *           scales [16 rows][head_dim / 16]
+ *   values  codes [head_dim / 8][16 rows][4];  scales [head_dim / 16][16 rows].
+ * head_dim 64, 128 or 256, block_size 16.  The tensor scales are positive and
+ * finite; largest magnitude / (6 * 448) uses the whole range of the scales.
+ * Block copies: pkv_copy_blocks with PKV_FP4_E2M1.
+ *
+ * pkv_kv_append_fp4 -- quantise and write the new rows.  For the 16 values x of
+ * a block, in IEEE float32, t the tensor scale:
+ *   A = max |x|,  s = E4M3(A / t / 6),  code = E2M1(x / (s * t)),
+ * rounded to nearest even and saturating (s at 448, codes at 6).  A block whose
+ * s is 0 is stored as zeros; one that holds a NaN gets a NaN scale and codes 0.
+ * k_new, v_new: [num_tokens, num_kv_heads, head_dim] of src_dtype
+ * (F32/BF16/F16); slots and errors as for pkv_kv_append.
+ */
+PKV_API pkv_status pkv_kv_append_fp4(const void *k_new, const void *v_new, void *k_cache,
+                                     void *v_cache, const int64_t *slot_mapping,
+                                     int64_t num_tokens, int num_kv_heads, int head_dim,
+                                     int block_size, int64_t num_blocks, pkv_dtype src_dtype,
+                                     float k_scale, float v_scale, int32_t *error_word,
+                                     pkv_stream_t stream);
+
+/*
+ * pkv_kv_load_fp4 -- rows of a 4-bit cache read back:  (code * s) * t, the
+ * product in brackets exact, rounded to float32 and then to out_dtype
+ * (F32/BF16/F16).  k_out, v_out: [num_tokens, num_kv_heads, head_dim], device;
+ * row i is the row in slot slot_mapping[i].  Slots < 0 (padding) give zeros, and
+ * so do slots past the cache, which are recorded (PKV_DEVERR_SLOT); a slot may
+ * be named more than once.
+ */
+PKV_API pkv_status pkv_kv_load_fp4(void *k_out, void *v_out, const void *k_cache,
+                                   const void *v_cache, const int64_t *slot_mapping,
+                                   int64_t num_tokens, int num_kv_heads, int head_dim,
+                                   int block_size, int64_t num_blocks, pkv_dtype out_dtype,
+                                   float k_scale, float v_scale, int32_t *error_word,
+                                   pkv_stream_t stream);
+
+/*
+ * pkv_paged_attention_fp4 -- decode (num_queries = 1), causal verification, or
+ * (tree_mask given) tree verification over 4-bit caches: the attention of
+ * pkv_spec_verify_attention / pkv_tree_verify_attention with the key and value
+ * elements as above.  q and out are of q_dtype (F32/BF16/F16), [batch,
+ * num_queries, num_heads, head_dim]; tree_mask and mask_batch_stride as for
+ * pkv_tree_verify_attention (NULL, 0: causal).  Plans and workspace sizes: the
+ * plan and workspace functions with dtype PKV_FP4_E2M1 (the plan is the one for
+ * 16-bit q; the workspace size covers float32 q too).  options: kernel,
+ * split_blocks, rows_per_cta, merge and split_waves; the others must be 0.
+ */
+PKV_API pkv_status pkv_paged_attention_fp4(
+    void *out, const void *q, const void *k_cache, const void *v_cache,
+    const int32_t *block_table, int max_blocks_per_seq,
+    const int32_t *context_lens, int max_context_len, int batch,
+    int num_queries, int num_heads, int num_kv_heads, int head_dim,
+    int block_size, int64_t num_blocks, float scale, pkv_dtype q_dtype,
+    float k_scale, float v_scale, const uint64_t *tree_mask,
+    int64_t mask_batch_stride, void *workspace, size_t workspace_bytes,
+    const pkv_options *options, int32_t *error_word, pkv_stream_t stream);
+
+/*
+ * pkv_commit_rows -- keep the accepted path of a verified tree.  The tree's
+ * num_queries nodes occupy the last rows of each sequence (node k at row
+ * L_b - num_queries + k, see pkv_tree_verify_attention); the accepted nodes
+ * path[b, 0 .. n_b) become rows L_b - num_queries .. L_b - num_queries + n_b - 1
+ * in every given cache tensor, and the sequence's length L_b - num_queries +
+ * n_b.  The rows after those keep whatever they hold.
+ *   k_caches, v_caches : HOST arrays of num_layers (<= 512) device pointers,
+ *                  every one a cache of the same sizes and dtype (any cache
+ *                  type); the tensors must not overlap.  v_caches NULL: one
+ *                  tensor per layer (MLA latents: one KV head, head_dim = width)
+ *   path         : device int32 [batch, max_path], strictly increasing node
+ *                  numbers in [0, num_queries) (entries past n_b unread);
+ *                  max_path and num_queries <= 64
+ *   path_lens    : device int32 [batch], 0 <= n_b <= min(max_path, num_queries)
+ *   new_lens     : NULL, or device int32 [batch]: the new lengths; must not
+ *                  overlap context_lens
+ * The moved rows must be in blocks that no other sequence of the batch uses
+ * (copy-on-write first).  A sequence whose path breaks its rules, or whose
+ * length is below num_queries or past the table, keeps its rows and length and
+ * is recorded (PKV_DEVERR_PATH, PKV_DEVERR_CONTEXT_LEN); a row whose block id
+ * is out of range is left out and recorded (PKV_DEVERR_BLOCK_ID).
+ * head_dim * sizeof(elt) must be a multiple of 16; 4-bit caches: 64, 128 or 256.
+ */
+PKV_API pkv_status pkv_commit_rows(void *const *k_caches, void *const *v_caches, int num_layers,
+                                   const int32_t *block_table, int max_blocks_per_seq,
+                                   const int32_t *context_lens, const int32_t *path, int max_path,
+                                   const int32_t *path_lens, int batch, int num_queries,
+                                   int num_kv_heads, int head_dim, int block_size,
+                                   int64_t num_blocks, pkv_dtype dtype, int32_t *new_lens,
+                                   int32_t *error_word, pkv_stream_t stream);
 
 /*
  * Multi-head latent attention (MLA) decode.  "Inference part 1", section

@@ -8,7 +8,9 @@ been built, or a call fails, an exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional
@@ -23,9 +25,9 @@ _lib = None
 PKV_KERNEL_AUTO, PKV_KERNEL_SIMT, PKV_KERNEL_MMA, PKV_KERNEL_TC = 0, 1, 2, 3
 DEVERR_NAMES = {0: "none", 1: "slot out of range", 2: "block id out of range",
                 3: "context length over max_context_len or the table",
-                4: "shared-memory copy timed out"}
+                4: "shared-memory copy timed out", 5: "accepted path not increasing tree nodes"}
 _DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-PKV_FP8_E4M3 = 3
+PKV_FP8_E4M3, PKV_FP4_E2M1 = 3, 4
 
 # Every symbol include/pkv.h declares.
 EXPORTED = ("pkv_status_string", "pkv_version", "pkv_kv_append", "pkv_attention_plan",
@@ -39,7 +41,8 @@ EXPORTED = ("pkv_status_string", "pkv_version", "pkv_kv_append", "pkv_attention_
             "pkv_copy_blocks", "pkv_paged_prefill_attention", "pkv_check_bounded_wait",
             "pkv_host_step_staging_size", "pkv_append_attention_host",
             "pkv_mla_plan", "pkv_mla_workspace_size", "pkv_mla_decode_attention",
-            "pkv_mla_append")
+            "pkv_mla_append", "pkv_kv_append_fp4", "pkv_kv_load_fp4", "pkv_paged_attention_fp4",
+            "pkv_commit_rows")
 
 
 class PkvError(RuntimeError):
@@ -134,6 +137,14 @@ def lib() -> ctypes.CDLL:
             L.pkv_paged_attention_fp8.argtypes = [vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32,
                                                   i32, i32, i32, i64, f32, i32, f32, f32, vp, sz,
                                                   opt, vp, vp]
+            L.pkv_kv_append_fp4.argtypes = L.pkv_kv_append_fp8.argtypes
+            L.pkv_kv_load_fp4.argtypes = L.pkv_kv_append_fp8.argtypes
+            L.pkv_paged_attention_fp4.argtypes = [vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32,
+                                                  i32, i32, i32, i64, f32, i32, f32, f32, vp, i64,
+                                                  vp, sz, opt, vp, vp]
+            L.pkv_commit_rows.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(vp), i32, vp, i32, vp,
+                                          vp, i32, vp, i32, i32, i32, i32, i32, i64, i32, vp, vp,
+                                          vp]
             L.pkv_paged_decode_attention_noalloc.argtypes = [vp, vp, vp, vp, vp, i32, vp, i32,
                                                              i32, i32, i32, i32, i32, i64, f32,
                                                              i32, opt, vp, vp]
@@ -239,9 +250,11 @@ def kv_append(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor,
 
 def _plan_dtype(dtype) -> int:
     """Plan/workspace element type: a torch dtype of q and cache, or
-    torch.uint8 / "fp8" for an FP8 E4M3 cache."""
+    torch.uint8 / "fp8" for an FP8 E4M3 cache, "fp4" for a 4-bit one."""
     if dtype in (torch.uint8, "fp8"):
         return PKV_FP8_E4M3
+    if dtype == "fp4":
+        return PKV_FP4_E2M1
     return _DTYPE[dtype]
 
 
@@ -657,6 +670,222 @@ def paged_attention_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
         B, Q, Hq, Hkv, D, bs, NB, float(scale), _DTYPE[q.dtype], float(k_scale), float(v_scale),
         ws_ptr, ws_bytes, _opts(kernel, split_blocks, stages), _err_ptr(error_word), _stream(q)))
     return out
+
+
+# ---- block-scaled 4-bit caches ---------------------------------------------------
+def fp4_cache_shape(num_blocks: int, num_kv_heads: int, head_dim: int) -> tuple:
+    """Shape of a uint8 4-bit cache: one (block, KV head) tile of 16 rows is
+    9 * head_dim contiguous bytes, codes then scales (pkv_kv_append_fp4)."""
+    _need(head_dim in (64, 128, 256), "head_dim must be 64, 128 or 256")
+    return (num_blocks, num_kv_heads, 16, 9 * head_dim // 16)
+
+
+_NO_GUARD = contextlib.nullcontext()
+
+
+def _on_device(device_index: int):
+    """The library launches on the current device: make it the tensors' one."""
+    if torch.cuda.current_device() == device_index:
+        return _NO_GUARD
+    return torch.cuda.device(device_index)
+
+
+def _on_one_device(what: str, *tensors) -> int:
+    """The CUDA device index that all the tensors (None: absent) share."""
+    index = tensors[0].get_device()
+    _need(index >= 0 and all(t is None or t.get_device() == index for t in tensors),
+          f"{what} must be on one CUDA device")
+    return index
+
+
+def _fp4_cache_args(k_cache, v_cache):
+    _need(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and k_cache.dtype == torch.uint8
+          and v_cache.dtype == torch.uint8 and k_cache.is_contiguous() and v_cache.is_contiguous()
+          and k_cache.shape[2] == 16 and k_cache.shape[3] in (36, 72, 144),
+          "4-bit caches: contiguous uint8 [num_blocks, num_kv_heads, 16, 9 * head_dim / 16] "
+          "(fp4_cache_shape), head_dim 64, 128 or 256")
+    NB, Hkv, bs, row = k_cache.shape
+    return NB, Hkv, bs, row * 16 // 9
+
+
+def _slots_arg(slot_mapping, T):
+    _need(slot_mapping.dtype == torch.int64 and slot_mapping.shape == (T,)
+          and slot_mapping.is_contiguous(), "slot_mapping int64 [T]")
+
+
+def kv_append_fp4(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor,
+                  v_cache: torch.Tensor, slot_mapping: torch.Tensor, k_scale: float,
+                  v_scale: float, error_word: Optional[torch.Tensor] = None) -> None:
+    """Quantise k_new/v_new [T, Hkv, D] (float32/bf16/f16) into the 4-bit
+    caches (fp4_cache_shape) at their slots (pkv_kv_append_fp4)."""
+    NB, Hkv, bs, D = _fp4_cache_args(k_cache, v_cache)
+    T = k_new.shape[0]
+    _need(k_new.shape == (T, Hkv, D) and v_new.shape == (T, Hkv, D)
+          and k_new.dtype == v_new.dtype and k_new.dtype in _DTYPE
+          and k_new.is_contiguous() and v_new.is_contiguous(), "k_new/v_new [T, Hkv, D]")
+    _slots_arg(slot_mapping, T)
+    dev = _on_one_device("k_new, v_new, caches and slot_mapping", k_cache, v_cache, k_new, v_new,
+                         slot_mapping, error_word)
+    with _on_device(dev):
+        _check("pkv_kv_append_fp4", lib().pkv_kv_append_fp4(
+            k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            slot_mapping.data_ptr(), T, Hkv, D, bs, NB, _DTYPE[k_new.dtype], float(k_scale),
+            float(v_scale), _err_ptr(error_word), _stream(k_cache)))
+
+
+def kv_load_fp4(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping: torch.Tensor,
+                k_scale: float, v_scale: float, dtype: torch.dtype = torch.bfloat16,
+                k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None,
+                error_word: Optional[torch.Tensor] = None):
+    """The rows of slots ``slot_mapping`` [T] of the 4-bit caches as (k, v)
+    [T, Hkv, D] of ``dtype``; padding (negative slots) reads as zeros
+    (pkv_kv_load_fp4)."""
+    NB, Hkv, bs, D = _fp4_cache_args(k_cache, v_cache)
+    T = slot_mapping.shape[0]
+    _slots_arg(slot_mapping, T)
+    _need(dtype in _DTYPE, "dtype: float32, bfloat16 or float16")
+    if k_out is None:
+        k_out = torch.empty(T, Hkv, D, dtype=dtype, device=k_cache.device)
+    if v_out is None:
+        v_out = torch.empty(T, Hkv, D, dtype=dtype, device=k_cache.device)
+    for t in (k_out, v_out):
+        _need(t.shape == (T, Hkv, D) and t.dtype == dtype and t.is_contiguous(),
+              "k_out / v_out: contiguous [T, Hkv, D] of dtype")
+    dev = _on_one_device("caches, slot_mapping and outputs", k_cache, v_cache, slot_mapping,
+                         k_out, v_out, error_word)
+    with _on_device(dev):
+        _check("pkv_kv_load_fp4", lib().pkv_kv_load_fp4(
+            k_out.data_ptr(), v_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            slot_mapping.data_ptr(), T, Hkv, D, bs, NB, _DTYPE[dtype], float(k_scale),
+            float(v_scale), _err_ptr(error_word), _stream(k_cache)))
+    return k_out, v_out
+
+
+@functools.lru_cache(maxsize=1024)
+def _fp4_workspace(device_index: int, B: int, Q: int, Hq: int, Hkv: int, D: int, bs: int,
+                   max_context_len: int, options: tuple) -> int:
+    """Workspace bytes of a call on the current device (a function of sizes)."""
+    n = ctypes.c_size_t(0)
+    _check("pkv_attention_workspace_size", lib().pkv_attention_workspace_size(
+        B, Q, Hq, Hkv, D, bs, max_context_len, PKV_FP4_E2M1,
+        ctypes.byref(Options(*options)) if any(options) else None, ctypes.byref(n)))
+    return int(n.value)
+
+
+def paged_attention_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                        block_table: torch.Tensor, context_lens: torch.Tensor, k_scale: float,
+                        v_scale: float, scale: Optional[float] = None,
+                        max_context_len: Optional[int] = None,
+                        tree_mask: Optional[torch.Tensor] = None,
+                        out: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, kernel: int = 0,
+                        split_blocks: int = 0,
+                        error_word: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Decode (q [B, Hq, D]), causal verification (q [B, Q, Hq, D]) or, with
+    ``tree_mask`` (int64 [Q] or [B, Q], as for tree_verify_attention), tree
+    verification over 4-bit caches (pkv_paged_attention_fp4); out has q's shape
+    and type."""
+    NB, Hkv, bs, D = _fp4_cache_args(k_cache, v_cache)
+    _need(q.dim() in (3, 4) and q.is_contiguous() and q.dtype in _DTYPE and q.shape[-1] == D,
+          "q must be a contiguous [B, Hq, D] or [B, Q, Hq, D]")
+    B, Hq = q.shape[0], q.shape[-2]
+    Q = q.shape[1] if q.dim() == 4 else 1
+    _need(block_table.dtype == torch.int32 and block_table.dim() == 2
+          and block_table.shape[0] == B and block_table.is_contiguous(),
+          "block_table must be a contiguous int32 [batch, max_blocks_per_seq]")
+    _need(context_lens.dtype == torch.int32 and context_lens.shape == (B,)
+          and context_lens.is_contiguous(), "context_lens must be a contiguous int32 [batch]")
+    stride = 0
+    if tree_mask is not None:
+        _need(tree_mask.dtype == torch.int64 and tree_mask.is_contiguous()
+              and tree_mask.shape in ((Q,), (B, Q)), "tree_mask: int64 [Q] or [B, Q]")
+        stride = 0 if tree_mask.dim() == 1 else Q
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous(), "out")
+    dev = _on_one_device("q, caches, block_table, context_lens, tree_mask, out and workspace", q,
+                         k_cache, v_cache, block_table, context_lens, out, tree_mask, workspace,
+                         error_word)
+    if max_context_len is None:
+        max_context_len = int(context_lens.max().item()) if B else 0  # device read
+    options = (kernel, split_blocks, 0, TUNING.get("rows_per_cta", 0), TUNING.get("merge", 0), 0, 0,
+               0, TUNING.get("split_waves", 0))
+    with _on_device(dev):
+        if workspace is None:
+            need = _fp4_workspace(dev, B, Q, Hq, Hkv, D, bs, max_context_len, options)
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        _need(workspace is None or workspace.is_contiguous(), "workspace must be contiguous")
+        _check("pkv_paged_attention_fp4", lib().pkv_paged_attention_fp4(
+            out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            block_table.data_ptr(), block_table.shape[1], context_lens.data_ptr(),
+            max_context_len, B, Q, Hq, Hkv, D, bs, NB, 0.0 if scale is None else float(scale),
+            _DTYPE[q.dtype], float(k_scale), float(v_scale),
+            None if tree_mask is None else tree_mask.data_ptr(), stride,
+            None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel() * workspace.element_size(),
+            ctypes.byref(Options(*options)) if any(options) else None, _err_ptr(error_word),
+            _stream(q)))
+    return out
+
+
+# ---- the accepted path of a verified tree ------------------------------------------
+def commit_rows(k_caches, v_caches, block_table: torch.Tensor, context_lens: torch.Tensor,
+                path: torch.Tensor, path_lens: torch.Tensor, num_queries: int, fp4: bool = False,
+                new_lens: Optional[torch.Tensor] = None,
+                error_word: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Move the accepted nodes' rows of a verified tree together in every layer
+    (pkv_commit_rows): row L - num_queries + path[b, i] of sequence b becomes
+    row L - num_queries + i, for i < path_lens[b].  Returns the new lengths
+    L - num_queries + path_lens (int32 [B]).
+
+    k_caches, v_caches: lists of equally shaped caches, one per layer, [NB, Hkv,
+    16, D] (uint8: FP8 codes, or with ``fp4`` 4-bit caches of fp4_cache_shape);
+    MLA latents [NB, 16, W]: v_caches None.  path: int32 [B, max_path]."""
+    caches = list(k_caches) + (list(v_caches) if v_caches is not None else [])
+    n = len(k_caches)
+    _need(n >= 1 and len(caches) == (n if v_caches is None else 2 * n),
+          "k_caches / v_caches: one tensor per layer")
+    first = caches[0]
+    _need(first.dim() == 4 or (first.dim() == 3 and v_caches is None),
+          "caches: [NB, Hkv, 16, D], or latents [NB, 16, W] without v_caches")
+    shape, dtype = first.shape, first.dtype
+    _need(all(t.shape == shape and t.dtype == dtype and t.is_contiguous() for t in caches),
+          "caches must be contiguous and of one shape and dtype")
+    if fp4:
+        _need(v_caches is not None, "4-bit caches come as keys and values")
+        NB, Hkv, bs, D = _fp4_cache_args(first, first)
+        dt = PKV_FP4_E2M1
+    else:
+        _need(dtype in _DTYPE or dtype == torch.uint8, "cache dtype")
+        NB, bs, D = shape[0], shape[-2], shape[-1]
+        Hkv = shape[1] if first.dim() == 4 else 1
+        dt = PKV_FP8_E4M3 if dtype == torch.uint8 else _DTYPE[dtype]
+    B = context_lens.shape[0]
+    _need(block_table.dtype == torch.int32 and block_table.dim() == 2
+          and block_table.shape[0] == B and block_table.is_contiguous(),
+          "block_table must be a contiguous int32 [batch, max_blocks_per_seq]")
+    _need(context_lens.dtype == torch.int32 and context_lens.dim() == 1
+          and context_lens.is_contiguous(), "context_lens must be a contiguous int32 [batch]")
+    _need(path.dtype == torch.int32 and path.dim() == 2 and path.shape[0] == B
+          and path.is_contiguous(), "path must be a contiguous int32 [batch, max_path]")
+    _need(path_lens.dtype == torch.int32 and path_lens.shape == (B,)
+          and path_lens.is_contiguous(), "path_lens must be a contiguous int32 [batch]")
+    if new_lens is None:
+        new_lens = torch.empty_like(context_lens)
+    _need(new_lens.dtype == torch.int32 and new_lens.shape == (B,) and new_lens.is_contiguous(),
+          "new_lens must be a contiguous int32 [batch]")
+    dev = _on_one_device("caches, block_table, lengths and paths", block_table, context_lens,
+                         path, path_lens, new_lens, error_word, *caches)
+    ptrs = [t.data_ptr() for t in caches]
+    array = ctypes.c_void_p * n
+    with _on_device(dev):
+        _check("pkv_commit_rows", lib().pkv_commit_rows(
+            array(*ptrs[:n]), array(*ptrs[n:]) if v_caches is not None else None, n,
+            block_table.data_ptr(), block_table.shape[1], context_lens.data_ptr(),
+            path.data_ptr(), path.shape[1], path_lens.data_ptr(), B, int(num_queries), Hkv, D, bs,
+            NB, dt, new_lens.data_ptr(), _err_ptr(error_word), _stream(block_table)))
+    return new_lens
 
 
 def read_error_word(error_word: torch.Tensor) -> int:

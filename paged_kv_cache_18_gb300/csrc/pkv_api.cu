@@ -10,6 +10,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <functional>
 #include <mutex>
 
 #include "../../include/pkv.h"
@@ -42,7 +43,19 @@ int elt_bytes(pkv_dtype dt) { return dt == PKV_F32 ? 4 : (dt == PKV_FP8_E4M3 ? 1
 
 bool valid_dtype(int dt) { return dt == PKV_F32 || dt == PKV_BF16 || dt == PKV_F16; }
 
-bool valid_cache_dtype(int dt) { return valid_dtype(dt) || dt == PKV_FP8_E4M3; }
+// Cache types whose elements are codes: q and out have a 16- or 32-bit type of
+// their own.
+bool coded(int dt) { return dt == PKV_FP8_E4M3 || dt == PKV_FP4_E2M1; }
+
+bool valid_cache_dtype(int dt) { return valid_dtype(dt) || coded(dt); }
+
+// Bytes of one (block, KV head) tile.
+int64_t tile_bytes(pkv_dtype dt, int64_t block_size, int64_t head_dim) {
+  if (dt == PKV_FP4_E2M1) return head_dim * 9 * block_size / 16;
+  return block_size * head_dim * elt_bytes(dt);
+}
+
+bool valid_tensor_scale(float s) { return s > 0.f && std::isfinite(s); }
 
 int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
@@ -111,7 +124,7 @@ cudaError_t prepare_kernel(const KernelInfo &k, int device, int *ctas_per_sm) {
 }
 
 // dtype is the cache's element type, qdtype that of q and out (equal unless
-// the cache is FP8 E4M3).
+// the cache holds FP8 or 4-bit codes).
 struct Shape {
   int batch, num_queries, num_heads, num_kv_heads, head_dim, block_size, max_context_len;
   pkv_dtype dtype;
@@ -120,8 +133,8 @@ struct Shape {
 
 Shape make_shape(int batch, int num_queries, int num_heads, int num_kv_heads, int head_dim,
                  int block_size, int max_context_len, pkv_dtype dtype) {
-  // Plans over an FP8 cache do not depend on q's type.
-  const pkv_dtype q = dtype == PKV_FP8_E4M3 ? PKV_BF16 : dtype;
+  // Plans over a cache of codes are those of 16-bit queries.
+  const pkv_dtype q = coded(dtype) ? PKV_BF16 : dtype;
   return Shape{batch, num_queries, num_heads, num_kv_heads, head_dim, block_size,
                max_context_len, dtype, q};
 }
@@ -131,7 +144,7 @@ pkv_status check_shape(const Shape &s) {
       s.head_dim < 1 || s.block_size < 1 || s.max_context_len < 0 ||
       !valid_cache_dtype(s.dtype) || !valid_dtype(s.qdtype))
     return PKV_ERR_INVALID_ARG;
-  if (s.dtype != PKV_FP8_E4M3 && s.qdtype != s.dtype) return PKV_ERR_INVALID_ARG;
+  if (!coded(s.dtype) && s.qdtype != s.dtype) return PKV_ERR_INVALID_ARG;
   if (s.dtype == PKV_FP8_E4M3 && s.head_dim != 128 && s.head_dim != 256)
     return PKV_ERR_UNSUPPORTED;
   if (s.num_heads % s.num_kv_heads != 0) return PKV_ERR_INVALID_ARG;
@@ -139,6 +152,32 @@ pkv_status check_shape(const Shape &s) {
   if (s.block_size != kBlockSize) return PKV_ERR_UNSUPPORTED;
   if (s.batch > 65535) return PKV_ERR_UNSUPPORTED;
   return PKV_OK;
+}
+
+// The same for a 4-bit cache.
+bool choose_fp4_kernel(const Shape &s, const pkv_options *opt, int rows, pkv_plan *pl,
+                       KernelInfo *info) {
+  int kernel = opt ? opt->kernel : PKV_KERNEL_AUTO;
+  if (opt && (opt->stages || opt->warp_tiles || opt->blocks_per_iter || opt->persistent))
+    return false;
+  if (kernel == PKV_KERNEL_AUTO) kernel = PKV_KERNEL_SIMT;
+  if (kernel != PKV_KERNEL_SIMT) return false;
+  int cap = simt_fp4_max_rows();
+  if (opt && opt->rows_per_cta > 0 && opt->rows_per_cta < cap) cap = opt->rows_per_cta;
+  const int chunks = ceil_div(rows, cap);
+  const int per_cta = ceil_div(rows, chunks);
+  int r = 1;
+  while (r < per_cta) r <<= 1;
+  if (!simt_fp4_kernel_info(s.qdtype, s.head_dim, r, info)) return false;
+  pl->kernel = kernel;
+  pl->rows_per_cta = per_cta;
+  pl->row_chunks = chunks;
+  pl->threads_per_cta = info->threads;
+  pl->stages = info->stages;
+  pl->smem_bytes = info->smem;
+  pl->warp_tiles = info->warp_tiles;
+  pl->blocks_per_iter = info->blocks_per_iter;
+  return true;
 }
 
 // Kernel family and per-CTA row tile.  Returns false if unsupported.
@@ -150,6 +189,7 @@ bool choose_kernel(const Shape &s, const pkv_options *opt, pkv_plan *pl, KernelI
   // against 0.974 for the CUDA-core kernel); float32 (cache or q) has no exact
   // tensor-core path.
   const bool f32 = s.dtype == PKV_F32 || s.qdtype == PKV_F32;
+  if (s.dtype == PKV_FP4_E2M1) return choose_fp4_kernel(s, opt, rows, pl, info);
   if (kernel == PKV_KERNEL_AUTO) kernel = f32 ? PKV_KERNEL_SIMT : PKV_KERNEL_MMA;
   if ((kernel == PKV_KERNEL_MMA || kernel == PKV_KERNEL_TC) && f32) return false;
   if (kernel == PKV_KERNEL_TC && s.dtype != s.qdtype) return false;
@@ -261,7 +301,8 @@ void plan_splits(const Shape &s, const pkv_options *opt, int num_sms, int ctas_p
   } else {
     const int64_t slots = static_cast<int64_t>(num_sms) * ctas_per_sm;
     const int64_t want = kTargetWaves * slots;
-    const int block_bytes = 2 * s.block_size * s.head_dim * elt_bytes(s.dtype);
+    const int block_bytes =
+        static_cast<int>(2 * tile_bytes(s.dtype, s.block_size, s.head_dim));
     const int max_unit_blocks = kMaxUnitBytes / block_bytes > 1 ? kMaxUnitBytes / block_bytes : 1;
     if (units >= want || max_blocks <= kMinSplitBlocks) {
       split_blocks = max_blocks;
@@ -490,7 +531,7 @@ pkv_status run_attention(void *out, const void *q, const void *k_cache, const vo
                          float k_scale = 1.f, float v_scale = 1.f, bool check_only = false) {
   pkv_status st = check_shape(s);
   if (st != PKV_OK) return st;
-  if (k_new && s.dtype == PKV_FP8_E4M3) return PKV_ERR_UNSUPPORTED;
+  if (k_new && coded(s.dtype)) return PKV_ERR_UNSUPPORTED;
   if (s.batch == 0) return PKV_OK;
   if (!out || !q || !k_cache || !v_cache || !block_table || !context_lens)
     return PKV_ERR_INVALID_ARG;
@@ -591,6 +632,10 @@ pkv_status run_attention(void *out, const void *q, const void *k_cache, const vo
         !encode_cache_map(&vmap, v_cache, s.dtype, s.head_dim, s.num_kv_heads, num_blocks))
       return PKV_ERR_CUDA;
     e = tc_launch(s.dtype, s.head_dim, pl.rows_per_cta, pl.stages, kmap, vmap, p, grid, stream);
+  } else if (s.dtype == PKV_FP4_E2M1) {
+    int r = 1;
+    while (r < pl.rows_per_cta) r <<= 1;
+    e = simt_fp4_launch(s.qdtype, s.head_dim, r, p, grid, stream);
   } else {
     int r = 1;
     while (r < pl.rows_per_cta) r <<= 1;
@@ -603,6 +648,29 @@ pkv_status run_attention(void *out, const void *q, const void *k_cache, const vo
   }
   return PKV_OK;
 }
+
+bool fp4_head_dim(int head_dim) { return head_dim == 64 || head_dim == 128 || head_dim == 256; }
+
+// The arguments of the 4-bit cache's append (rows in) and load (rows out).
+pkv_status check_fp4_rows(const void *k_rows, const void *v_rows, const void *k_cache,
+                          const void *v_cache, const int64_t *slots, int64_t num_tokens,
+                          int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                          pkv_dtype row_dtype, float k_scale, float v_scale,
+                          const int32_t *error_word) {
+  if (num_tokens < 0 || num_kv_heads < 1 || head_dim < 1 || block_size < 1 || num_blocks < 1 ||
+      !valid_dtype(row_dtype) || !valid_tensor_scale(k_scale) || !valid_tensor_scale(v_scale))
+    return PKV_ERR_INVALID_ARG;
+  if (!fp4_head_dim(head_dim) || block_size != kBlockSize) return PKV_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return PKV_OK;
+  if (!k_rows || !v_rows || !k_cache || !v_cache || !slots) return PKV_ERR_INVALID_ARG;
+  if (!aligned(k_rows, 16) || !aligned(v_rows, 16) || !aligned(k_cache, 16) ||
+      !aligned(v_cache, 16) || !aligned(slots, 8) || !aligned(error_word, 4))
+    return PKV_ERR_ALIGNMENT;
+  return PKV_OK;
+}
+
+// Layers of one commit call (the list of tensors is checked on the host).
+constexpr int kMaxCommitLayers = 512;
 
 }  // namespace
 }  // namespace pkv
@@ -658,8 +726,9 @@ pkv_status pkv_copy_blocks(void *k_cache, void *v_cache, const int32_t *src, con
     return PKV_ERR_INVALID_ARG;
   if (num_pairs == 0) return PKV_OK;
   if (!k_cache || !v_cache || !src || !dst) return PKV_ERR_INVALID_ARG;
-  const int64_t block_bytes =
-      static_cast<int64_t>(num_kv_heads) * block_size * head_dim * elt_bytes(dtype);
+  if (dtype == PKV_FP4_E2M1 && (head_dim % 16 != 0 || block_size != kBlockSize))
+    return PKV_ERR_UNSUPPORTED;
+  const int64_t block_bytes = num_kv_heads * tile_bytes(dtype, block_size, head_dim);
   if (block_bytes % 16 != 0) return PKV_ERR_UNSUPPORTED;
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(src, 4) || !aligned(dst, 4) ||
       (error_word && !aligned(error_word, 4)))
@@ -795,8 +864,8 @@ pkv_status pkv_attention_workspace_size(int batch, int num_queries, int num_head
                                            block_size, max_context_len, dtype, options, &pl);
   if (st != PKV_OK) return st;
   *bytes = pl.workspace_bytes;
-  if (dtype == PKV_FP8_E4M3 && (!options || options->kernel != PKV_KERNEL_MMA)) {
-    // float32 queries over an FP8 cache take the CUDA-core kernel: report
+  if (coded(dtype) && (!options || options->kernel != PKV_KERNEL_MMA)) {
+    // float32 queries over a cache of codes take the CUDA-core kernel: report
     // enough for either plan.
     Shape s = make_shape(batch, num_queries, num_heads, num_kv_heads, head_dim, block_size,
                          max_context_len, dtype);
@@ -820,7 +889,7 @@ pkv_status pkv_paged_decode_attention(void *out, const void *q, const void *k_ca
                                       void *workspace, size_t workspace_bytes,
                                       const pkv_options *options, int32_t *error_word,
                                       pkv_stream_t stream) {
-  if (dtype == PKV_FP8_E4M3) return PKV_ERR_INVALID_ARG;  // pkv_paged_attention_fp8
+  if (coded(dtype)) return PKV_ERR_INVALID_ARG;  // pkv_paged_attention_fp8 / _fp4
   const Shape s = make_shape(batch, 1, num_heads, num_kv_heads, head_dim, block_size, max_context_len, dtype);
   return run_attention(out, q, k_cache, v_cache, block_table, max_blocks_per_seq, context_lens, s,
                        num_blocks, scale, workspace, workspace_bytes, options, error_word,
@@ -836,7 +905,7 @@ pkv_status pkv_spec_verify_attention(void *out, const void *q, const void *k_cac
                                      pkv_dtype dtype, void *workspace, size_t workspace_bytes,
                                      const pkv_options *options, int32_t *error_word,
                                      pkv_stream_t stream) {
-  if (dtype == PKV_FP8_E4M3) return PKV_ERR_INVALID_ARG;  // pkv_paged_attention_fp8
+  if (coded(dtype)) return PKV_ERR_INVALID_ARG;  // pkv_paged_attention_fp8 / _fp4
   const Shape s = make_shape(batch, num_queries, num_heads, num_kv_heads, head_dim, block_size,
                 max_context_len, dtype);
   return run_attention(out, q, k_cache, v_cache, block_table, max_blocks_per_seq, context_lens, s,
@@ -852,7 +921,7 @@ pkv_status pkv_append_attention(void *out, const void *q, const void *k_new, con
                                 float scale, pkv_dtype dtype, void *workspace,
                                 size_t workspace_bytes, const pkv_options *options,
                                 int32_t *error_word, pkv_stream_t stream) {
-  if (dtype == PKV_FP8_E4M3) return PKV_ERR_INVALID_ARG;  // pkv_paged_attention_fp8
+  if (coded(dtype)) return PKV_ERR_INVALID_ARG;  // pkv_paged_attention_fp8 / _fp4
   if (batch > 0 && (!k_new || !v_new)) return PKV_ERR_INVALID_ARG;
   const Shape s = make_shape(batch, num_queries, num_heads, num_kv_heads, head_dim, block_size,
                 max_context_len, dtype);
@@ -1051,7 +1120,7 @@ pkv_status pkv_tree_verify_attention(void *out, const void *q, const void *k_cac
                                      int64_t mask_batch_stride, void *workspace,
                                      size_t workspace_bytes, const pkv_options *options,
                                      int32_t *error_word, pkv_stream_t stream) {
-  if (dtype == PKV_FP8_E4M3) return PKV_ERR_INVALID_ARG;  // pkv_paged_attention_fp8
+  if (coded(dtype)) return PKV_ERR_INVALID_ARG;  // pkv_paged_attention_fp8 / _fp4
   if (num_queries > 64 || mask_batch_stride < 0) return PKV_ERR_INVALID_ARG;
   if (batch > 0 && !tree_mask) return PKV_ERR_INVALID_ARG;
   if (!aligned(tree_mask, 8)) return PKV_ERR_ALIGNMENT;
@@ -1106,6 +1175,141 @@ pkv_status pkv_paged_attention_fp8(void *out, const void *q, const void *k_cache
                        num_blocks, scale, workspace, workspace_bytes, options, error_word,
                        reinterpret_cast<cudaStream_t>(stream), nullptr, nullptr, nullptr, 0,
                        k_scale, v_scale);
+}
+
+pkv_status pkv_kv_append_fp4(const void *k_new, const void *v_new, void *k_cache, void *v_cache,
+                             const int64_t *slot_mapping, int64_t num_tokens, int num_kv_heads,
+                             int head_dim, int block_size, int64_t num_blocks,
+                             pkv_dtype src_dtype, float k_scale, float v_scale,
+                             int32_t *error_word, pkv_stream_t stream) {
+  const pkv_status st = check_fp4_rows(k_new, v_new, k_cache, v_cache, slot_mapping, num_tokens,
+                                       num_kv_heads, head_dim, block_size, num_blocks, src_dtype,
+                                       k_scale, v_scale, error_word);
+  if (st != PKV_OK || num_tokens == 0) return st;
+  int device = 0, sms = 0;
+  if (current_sm_count(&device, &sms) != cudaSuccess) return PKV_ERR_CUDA;
+  const cudaError_t e = append_fp4_launch(src_dtype, k_new, v_new, k_cache, v_cache, slot_mapping,
+                                          num_tokens, num_kv_heads, head_dim, num_blocks, k_scale,
+                                          v_scale, error_word, sms,
+                                          reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_kv_load_fp4(void *k_out, void *v_out, const void *k_cache, const void *v_cache,
+                           const int64_t *slot_mapping, int64_t num_tokens, int num_kv_heads,
+                           int head_dim, int block_size, int64_t num_blocks, pkv_dtype out_dtype,
+                           float k_scale, float v_scale, int32_t *error_word,
+                           pkv_stream_t stream) {
+  const pkv_status st = check_fp4_rows(k_out, v_out, k_cache, v_cache, slot_mapping, num_tokens,
+                                       num_kv_heads, head_dim, block_size, num_blocks, out_dtype,
+                                       k_scale, v_scale, error_word);
+  if (st != PKV_OK || num_tokens == 0) return st;
+  int device = 0, sms = 0;
+  if (current_sm_count(&device, &sms) != cudaSuccess) return PKV_ERR_CUDA;
+  const cudaError_t e = load_fp4_launch(out_dtype, k_out, v_out, k_cache, v_cache, slot_mapping,
+                                        num_tokens, num_kv_heads, head_dim, num_blocks, k_scale,
+                                        v_scale, error_word, sms,
+                                        reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_paged_attention_fp4(void *out, const void *q, const void *k_cache,
+                                   const void *v_cache, const int32_t *block_table,
+                                   int max_blocks_per_seq, const int32_t *context_lens,
+                                   int max_context_len, int batch, int num_queries, int num_heads,
+                                   int num_kv_heads, int head_dim, int block_size,
+                                   int64_t num_blocks, float scale, pkv_dtype q_dtype,
+                                   float k_scale, float v_scale, const uint64_t *tree_mask,
+                                   int64_t mask_batch_stride, void *workspace,
+                                   size_t workspace_bytes, const pkv_options *options,
+                                   int32_t *error_word, pkv_stream_t stream) {
+  if (!valid_dtype(q_dtype) || !valid_tensor_scale(k_scale) || !valid_tensor_scale(v_scale))
+    return PKV_ERR_INVALID_ARG;
+  if (tree_mask && (num_queries > 64 || mask_batch_stride < 0)) return PKV_ERR_INVALID_ARG;
+  if (!aligned(tree_mask, 8)) return PKV_ERR_ALIGNMENT;
+  Shape s = make_shape(batch, num_queries, num_heads, num_kv_heads, head_dim, block_size,
+                       max_context_len, PKV_FP4_E2M1);
+  s.qdtype = q_dtype;
+  return run_attention(out, q, k_cache, v_cache, block_table, max_blocks_per_seq, context_lens, s,
+                       num_blocks, scale, workspace, workspace_bytes, options, error_word,
+                       reinterpret_cast<cudaStream_t>(stream), nullptr, nullptr, tree_mask,
+                       mask_batch_stride, k_scale, v_scale);
+}
+
+pkv_status pkv_commit_rows(void *const *k_caches, void *const *v_caches, int num_layers,
+                           const int32_t *block_table, int max_blocks_per_seq,
+                           const int32_t *context_lens, const int32_t *path, int max_path,
+                           const int32_t *path_lens, int batch, int num_queries,
+                           int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                           pkv_dtype dtype, int32_t *new_lens, int32_t *error_word,
+                           pkv_stream_t stream) {
+  if (num_layers < 1 || batch < 0 || num_queries < 1 || num_queries > 64 || max_path < 1 ||
+      max_path > 64 || num_kv_heads < 1 || head_dim < 1 || block_size < 1 || num_blocks < 1 ||
+      max_blocks_per_seq < 1 || !valid_cache_dtype(dtype))
+    return PKV_ERR_INVALID_ARG;
+  if (num_layers > kMaxCommitLayers) return PKV_ERR_UNSUPPORTED;
+  if (block_size != kBlockSize || num_blocks > (int64_t(1) << 31)) return PKV_ERR_UNSUPPORTED;
+  const bool fp4 = dtype == PKV_FP4_E2M1;
+  const int64_t row_bytes = static_cast<int64_t>(head_dim) * (fp4 ? 1 : elt_bytes(dtype));
+  if (fp4 ? !fp4_head_dim(head_dim) : row_bytes % 16 != 0) return PKV_ERR_UNSUPPORTED;
+  if (batch == 0) return PKV_OK;
+  if (!k_caches || !block_table || !context_lens || !path || !path_lens)
+    return PKV_ERR_INVALID_ARG;
+  if (!aligned(block_table, 4) || !aligned(context_lens, 4) || !aligned(path, 4) ||
+      !aligned(path_lens, 4) || !aligned(new_lens, 4) || !aligned(error_word, 4))
+    return PKV_ERR_ALIGNMENT;
+  // the lengths are read by every warp and written by one
+  const uintptr_t a = reinterpret_cast<uintptr_t>(new_lens),
+                  c = reinterpret_cast<uintptr_t>(context_lens), len = 4 * uintptr_t(batch);
+  if (new_lens && a < c + len && c < a + len) return PKV_ERR_INVALID_ARG;
+  // Every tensor once: a second move of the same rows would find them moved.
+  const int tensors = v_caches ? 2 * num_layers : num_layers;
+  const uint64_t cache_bytes =
+      static_cast<uint64_t>(num_blocks) * num_kv_heads * tile_bytes(dtype, block_size, head_dim);
+  const char *order[2 * kMaxCommitLayers];
+  for (int i = 0; i < tensors; ++i) {
+    const void *t = i < num_layers ? k_caches[i] : v_caches[i - num_layers];
+    if (!t) return PKV_ERR_INVALID_ARG;
+    if (!aligned(t, 16)) return PKV_ERR_ALIGNMENT;
+    order[i] = static_cast<const char *>(t);
+  }
+  std::sort(order, order + tensors, std::less<const char *>());
+  for (int i = 1; i < tensors; ++i)
+    if (reinterpret_cast<uintptr_t>(order[i]) - reinterpret_cast<uintptr_t>(order[i - 1]) <
+        cache_bytes)
+      return PKV_ERR_INVALID_ARG;
+
+  CommitParams p{};
+  p.block_table = block_table;
+  p.context_lens = context_lens;
+  p.path = path;
+  p.path_lens = path_lens;
+  p.new_lens = new_lens;
+  p.err = error_word;
+  p.num_blocks = num_blocks;
+  p.vec_per_row = row_bytes / 16;
+  p.columns = num_kv_heads * (fp4 ? int64_t(head_dim / 8 + head_dim / 16) : p.vec_per_row);
+  p.batch = batch;
+  p.num_queries = num_queries;
+  p.heads = num_kv_heads;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.max_path = max_path;
+  const int per_launch = v_caches ? kMaxCommit / 2 : kMaxCommit;
+  for (int l0 = 0; l0 < num_layers; l0 += per_launch) {
+    const int n = std::min(per_launch, num_layers - l0);
+    CommitList list{};
+    for (int i = 0; i < n; ++i) {
+      list.cache[i] = k_caches[l0 + i];
+      if (v_caches) list.cache[n + i] = v_caches[l0 + i];
+    }
+    list.count = v_caches ? 2 * n : n;
+    list.first_value = n;
+    if (commit_launch(list, p, fp4 ? head_dim : 0, reinterpret_cast<cudaStream_t>(stream)) !=
+        cudaSuccess)
+      return PKV_ERR_CUDA;
+    p.new_lens = nullptr;  // written once
+  }
+  return PKV_OK;
 }
 
 }  // extern "C"

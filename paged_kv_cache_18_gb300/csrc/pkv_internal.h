@@ -96,6 +96,44 @@ cudaError_t append_fp8_launch(pkv_dtype src_dtype, const void *k_new, const void
                               int64_t num_blocks, float k_scale, float v_scale, int32_t *err,
                               int sm_count, cudaStream_t stream);
 
+// Rows into and out of a block-scaled 4-bit cache (kv_fp4.cu); head_dim 64, 128
+// or 256.
+cudaError_t append_fp4_launch(pkv_dtype src_dtype, const void *k_new, const void *v_new,
+                              void *k_cache, void *v_cache, const int64_t *slots,
+                              int64_t num_tokens, int num_kv_heads, int head_dim,
+                              int64_t num_blocks, float k_scale, float v_scale, int32_t *err,
+                              int sm_count, cudaStream_t stream);
+cudaError_t load_fp4_launch(pkv_dtype out_dtype, void *k_out, void *v_out, const void *k_cache,
+                            const void *v_cache, const int64_t *slots, int64_t num_tokens,
+                            int num_kv_heads, int head_dim, int64_t num_blocks, float k_scale,
+                            float v_scale, int32_t *err, int sm_count, cudaStream_t stream);
+
+// CUDA-core attention over a 4-bit cache (attn_simt_fp4.cu): rows = query rows
+// per CTA, 1, 2 or 4.
+int simt_fp4_max_rows();
+bool simt_fp4_kernel_info(pkv_dtype q_dtype, int head_dim, int rows, KernelInfo *info);
+cudaError_t simt_fp4_launch(pkv_dtype q_dtype, int head_dim, int rows, const AttnParams &p,
+                            dim3 grid, cudaStream_t stream);
+
+// Row moves after a verified tree (commit_rows.cu): every cache tensor of a
+// list in one launch; the first `first_value` of it hold keys (the 4-bit tiles
+// differ).  fp4_head_dim: 0 for plain rows of vec_per_row 16-byte vectors.
+constexpr int kMaxCommit = 128;
+struct CommitList {
+  void *cache[kMaxCommit];
+  int count, first_value;
+};
+struct CommitParams {
+  const int32_t *block_table, *context_lens, *path, *path_lens;
+  int32_t *new_lens, *err;
+  int64_t num_blocks, vec_per_row;
+  int64_t columns;        // units of a row over all heads
+  int64_t warps_per_seq;  // set by the launcher
+  int batch, num_queries, heads, max_blocks_per_seq, max_path;
+};
+cudaError_t commit_launch(const CommitList &list, CommitParams p, int fp4_head_dim,
+                          cudaStream_t stream);
+
 // Whole-block copies (copy-on-write) in both caches.
 cudaError_t copy_blocks_launch(void *k_cache, void *v_cache, const int32_t *src,
                                const int32_t *dst, int num_pairs, int64_t block_bytes,
