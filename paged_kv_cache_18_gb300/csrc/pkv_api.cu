@@ -160,15 +160,19 @@ bool choose_fp4_kernel(const Shape &s, const pkv_options *opt, int rows, pkv_pla
   int kernel = opt ? opt->kernel : PKV_KERNEL_AUTO;
   if (opt && (opt->stages || opt->warp_tiles || opt->blocks_per_iter || opt->persistent))
     return false;
-  if (kernel == PKV_KERNEL_AUTO) kernel = PKV_KERNEL_SIMT;
-  if (kernel != PKV_KERNEL_SIMT) return false;
-  int cap = simt_fp4_max_rows();
+  const bool f32 = s.qdtype == PKV_F32;  // no exact tensor-core path
+  if (kernel == PKV_KERNEL_AUTO) kernel = f32 ? PKV_KERNEL_SIMT : PKV_KERNEL_MMA;
+  if (kernel != PKV_KERNEL_SIMT && (kernel != PKV_KERNEL_MMA || f32)) return false;
+  const bool mma = kernel == PKV_KERNEL_MMA;
+  int cap = mma ? 8 * mma_fp4_max_tiles(s.head_dim) : simt_fp4_max_rows();
   if (opt && opt->rows_per_cta > 0 && opt->rows_per_cta < cap) cap = opt->rows_per_cta;
   const int chunks = ceil_div(rows, cap);
   const int per_cta = ceil_div(rows, chunks);
   int r = 1;
   while (r < per_cta) r <<= 1;
-  if (!simt_fp4_kernel_info(s.qdtype, s.head_dim, r, info)) return false;
+  if (mma ? !mma_fp4_kernel_info(s.qdtype, s.head_dim, ceil_div(per_cta, 8), info)
+          : !simt_fp4_kernel_info(s.qdtype, s.head_dim, r, info))
+    return false;
   pl->kernel = kernel;
   pl->rows_per_cta = per_cta;
   pl->row_chunks = chunks;
@@ -615,7 +619,9 @@ pkv_status run_attention(void *out, const void *q, const void *k_cache, const vo
                              stream);
     if (e != cudaSuccess) return PKV_ERR_CUDA;
   }
-  if (pl.kernel == PKV_KERNEL_MMA) {
+  if (pl.kernel == PKV_KERNEL_MMA && s.dtype == PKV_FP4_E2M1) {
+    e = mma_fp4_launch(s.qdtype, s.head_dim, ceil_div(pl.rows_per_cta, 8), p, grid, stream);
+  } else if (pl.kernel == PKV_KERNEL_MMA) {
     CUtensorMap kmap, vmap;
     p.tile_box =
         encode_cache_tile_map(&kmap, k_cache, s.dtype, s.head_dim, s.num_kv_heads, num_blocks) &&

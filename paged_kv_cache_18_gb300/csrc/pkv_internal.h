@@ -115,6 +115,13 @@ bool simt_fp4_kernel_info(pkv_dtype q_dtype, int head_dim, int rows, KernelInfo 
 cudaError_t simt_fp4_launch(pkv_dtype q_dtype, int head_dim, int rows, const AttnParams &p,
                             dim3 grid, cudaStream_t stream);
 
+// Tensor-core attention over a 4-bit cache (attn_fp4.cu): bf16 / f16 q, `tiles`
+// 8-column tiles of query rows per CTA.
+int mma_fp4_max_tiles(int head_dim);
+bool mma_fp4_kernel_info(pkv_dtype q_dtype, int head_dim, int tiles, KernelInfo *info);
+cudaError_t mma_fp4_launch(pkv_dtype q_dtype, int head_dim, int tiles, const AttnParams &p,
+                           dim3 grid, cudaStream_t stream);
+
 // Row moves after a verified tree (commit_rows.cu): every cache tensor of a
 // list in one launch; the first `first_value` of it hold keys (the 4-bit tiles
 // differ).  fp4_head_dim: 0 for plain rows of vec_per_row 16-byte vectors.
