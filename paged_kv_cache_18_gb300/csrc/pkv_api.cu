@@ -35,6 +35,12 @@ constexpr int kMaxSplits = 32;          // per sequence: each split adds merge w
 // first chunk's scores, the epilogue: ~5 us against ~0.2 us a block on the
 // verify step).
 constexpr int kStreamKWeight = 24;
+// The same for the 4-bit cache's tensor-core kernel (a CTA's four warps start
+// and finish a piece in about the time of this many blocks), the fewest blocks
+// worth a CTA, and the longest batch whose lengths every CTA adds up.
+constexpr int kFp4Weight = 8;
+constexpr int kFp4MinBlocks = 16;
+constexpr int kFp4MaxBatch = 1024;
 constexpr size_t kUsableSmemPerSm = 228 * 1024;
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -290,6 +296,26 @@ void plan_splits(const Shape &s, const pkv_options *opt, int num_sms, int ctas_p
   const int64_t units =
       static_cast<int64_t>(s.batch) * s.num_kv_heads * static_cast<int64_t>(pl->row_chunks);
   const bool persistent = pl->kernel == PKV_KERNEL_TC;
+  const bool fp4_mma = s.dtype == PKV_FP4_E2M1 && pl->kernel == PKV_KERNEL_MMA;
+  pl->stream_k = 0;
+  if (fp4_mma && !(opt && (opt->split_blocks > 0 || opt->split_waves != 0 || opt->merge == 1)) &&
+      s.batch <= kFp4MaxBatch && max_blocks > kMinSplitBlocks &&
+      units * (max_blocks + kFp4Weight) < (int64_t(1) << 31)) {  // int offsets on device
+    // The balanced partition: every resident CTA the same number of blocks.
+    const int64_t slots = static_cast<int64_t>(num_sms) * ctas_per_sm;
+    const int64_t most = (units * max_blocks + kFp4MinBlocks - 1) / kFp4MinBlocks;
+    pl->split_target = static_cast<int>(std::max<int64_t>(1, std::min(slots, most)));
+    pl->stream_k = 1;
+    pl->split_blocks = 0;
+    pl->num_splits = std::min(pl->split_target, max_blocks);
+    pl->grid_x = pl->split_target;
+    pl->grid_y = pl->grid_z = 1;
+    pl->ctas_per_sm = ctas_per_sm;
+    pl->workspace_bytes = workspace_layout(s, pl->num_splits, pl->row_chunks, pl->rows_per_cta, 2,
+                                           pl->split_target, 1).total;
+    pl->merge_kernel = 1;
+    return;
+  }
   int split_blocks;
   if (opt && opt->split_blocks > 0) {
     split_blocks = opt->split_blocks;
@@ -338,7 +364,6 @@ void plan_splits(const Shape &s, const pkv_options *opt, int num_sms, int ctas_p
   // kernels being bound by the bytes in flight rather than by idle slots.
   int waves = opt ? opt->split_waves : 0;
   const int64_t unit_rows = static_cast<int64_t>(s.num_kv_heads) * pl->row_chunks;
-  pl->stream_k = 0;
   // The tcgen05 kernel (one CTA per SM) takes the balanced partition by
   // default: every CTA the same number of blocks, whatever the lengths.  Any
   // whole-item partition leaves SMs idle at the end: the verify step's two
@@ -589,7 +614,7 @@ pkv_status run_attention(void *out, const void *q, const void *k_cache, const vo
   p.num_splits = pl.num_splits;
   p.split_target = pl.split_target;
   p.stream_k = pl.stream_k;
-  p.sk_weight = pl.stream_k ? kStreamKWeight : 0;
+  p.sk_weight = !pl.stream_k ? 0 : (s.dtype == PKV_FP4_E2M1 ? kFp4Weight : kStreamKWeight);
   p.scale_log2 =
       static_cast<float>(static_cast<double>(scale) * 1.4426950408889634 * k_scale);
   p.out_scale = v_scale;
