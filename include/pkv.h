@@ -491,7 +491,8 @@ PKV_API pkv_status pkv_kv_load_fp4(void *k_out, void *v_out, const void *k_cache
  * pkv_tree_verify_attention (NULL, 0: causal).  Plans and workspace sizes: the
  * plan and workspace functions with dtype PKV_FP4_E2M1 (the plan is the one for
  * 16-bit q; the workspace size covers float32 q too).  options: kernel,
- * split_blocks, rows_per_cta, merge and split_waves; the others must be 0.
+ * split_blocks, rows_per_cta and split_waves (merge 0 or 2); the others must
+ * be 0.
  */
 PKV_API pkv_status pkv_paged_attention_fp4(
     void *out, const void *q, const void *k_cache, const void *v_cache,

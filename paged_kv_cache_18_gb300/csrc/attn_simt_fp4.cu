@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kWarps * 32) simt_kernel(const AttnParams p) {
     }
   }
   __syncthreads();
-  cta_epilogue<TQ, D, R, kWarps, kWarps * 32>(p, red_m, red_l, red_o, wscale, wk);
+  cta_epilogue<TQ, D, R, kWarps, kWarps * 32, true>(p, red_m, red_l, red_o, wscale, wk);
 }
 
 template <int D, int R> constexpr size_t simt_smem() {

@@ -35,12 +35,14 @@ constexpr int kMaxSplits = 32;          // per sequence: each split adds merge w
 // first chunk's scores, the epilogue: ~5 us against ~0.2 us a block on the
 // verify step).
 constexpr int kStreamKWeight = 24;
-// The same for the 4-bit cache's tensor-core kernel (a CTA's four warps start
-// and finish a piece in about the time of this many blocks), the fewest blocks
-// worth a CTA, and the longest batch whose lengths every CTA adds up.
-constexpr int kFp4Weight = 8;
+// The same for the 4-bit cache's tensor-core kernel, its workers being CTAs or
+// warps, the fewest blocks worth a CTA, and the longest batch whose lengths
+// every worker adds up.
+constexpr int kFp4Weight = 32, kFp4WarpWeight = 8;
 constexpr int kFp4MinBlocks = 16;
 constexpr int kFp4MaxBatch = 1024;
+// Units from which its workers are warps.
+constexpr int64_t kFp4WarpUnits = 608;
 constexpr size_t kUsableSmemPerSm = 228 * 1024;
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -160,12 +162,31 @@ pkv_status check_shape(const Shape &s) {
   return PKV_OK;
 }
 
+// Whether a call over a 4-bit cache takes the balanced partition (its bounds:
+// launch controls for another one, lengths that every CTA adds up, int offsets
+// on the device).
+bool fp4_balanced(const Shape &s, const pkv_options *opt, int64_t units) {
+  const int max_blocks = ceil_div(s.max_context_len, s.block_size);
+  return !(opt && (opt->split_blocks > 0 || opt->split_waves != 0)) && s.batch <= kFp4MaxBatch && max_blocks > kMinSplitBlocks &&
+         units * (max_blocks + kFp4Weight) < (int64_t(1) << 31);
+}
+
+// With many units (sequence, KV head, row chunk) each warp is a worker of the
+// balanced partition: a unit is then cut into few pieces all the same, and a
+// piece costs a warp its start and end once instead of four warps.
+bool fp4_warp_workers(const Shape &s, const pkv_options *opt, int row_chunks, int rows) {
+  const int64_t units = static_cast<int64_t>(s.batch) * s.num_kv_heads * row_chunks;
+  return fp4_balanced(s, opt, units) && units >= kFp4WarpUnits &&
+         rows <= 8 * mma_fp4_max_warp_tiles(s.head_dim);
+}
+
 // The same for a 4-bit cache.
 bool choose_fp4_kernel(const Shape &s, const pkv_options *opt, int rows, pkv_plan *pl,
                        KernelInfo *info) {
   int kernel = opt ? opt->kernel : PKV_KERNEL_AUTO;
-  if (opt && (opt->stages || opt->warp_tiles || opt->blocks_per_iter || opt->persistent))
-    return false;
+  if (opt && (opt->stages || opt->warp_tiles || opt->blocks_per_iter || opt->persistent ||
+              opt->merge == 1))
+    return false;  // (splits are merged by the merge kernel)
   const bool f32 = s.qdtype == PKV_F32;  // no exact tensor-core path
   if (kernel == PKV_KERNEL_AUTO) kernel = f32 ? PKV_KERNEL_SIMT : PKV_KERNEL_MMA;
   if (kernel != PKV_KERNEL_SIMT && (kernel != PKV_KERNEL_MMA || f32)) return false;
@@ -176,7 +197,8 @@ bool choose_fp4_kernel(const Shape &s, const pkv_options *opt, int rows, pkv_pla
   const int per_cta = ceil_div(rows, chunks);
   int r = 1;
   while (r < per_cta) r <<= 1;
-  if (mma ? !mma_fp4_kernel_info(s.qdtype, s.head_dim, ceil_div(per_cta, 8), info)
+  if (mma ? !mma_fp4_kernel_info(s.qdtype, s.head_dim, ceil_div(per_cta, 8),
+                                 fp4_warp_workers(s, opt, chunks, per_cta), info)
           : !simt_fp4_kernel_info(s.qdtype, s.head_dim, r, info))
     return false;
   pl->kernel = kernel;
@@ -296,19 +318,20 @@ void plan_splits(const Shape &s, const pkv_options *opt, int num_sms, int ctas_p
   const int64_t units =
       static_cast<int64_t>(s.batch) * s.num_kv_heads * static_cast<int64_t>(pl->row_chunks);
   const bool persistent = pl->kernel == PKV_KERNEL_TC;
+  const bool separate_merge = persistent || s.dtype == PKV_FP4_E2M1;
   const bool fp4_mma = s.dtype == PKV_FP4_E2M1 && pl->kernel == PKV_KERNEL_MMA;
   pl->stream_k = 0;
-  if (fp4_mma && !(opt && (opt->split_blocks > 0 || opt->split_waves != 0 || opt->merge == 1)) &&
-      s.batch <= kFp4MaxBatch && max_blocks > kMinSplitBlocks &&
-      units * (max_blocks + kFp4Weight) < (int64_t(1) << 31)) {  // int offsets on device
-    // The balanced partition: every resident CTA the same number of blocks.
+  if (fp4_mma && fp4_balanced(s, opt, units)) {
+    // The balanced partition: every resident worker the same number of blocks.
     const int64_t slots = static_cast<int64_t>(num_sms) * ctas_per_sm;
     const int64_t most = (units * max_blocks + kFp4MinBlocks - 1) / kFp4MinBlocks;
-    pl->split_target = static_cast<int>(std::max<int64_t>(1, std::min(slots, most)));
+    pl->grid_x = static_cast<int>(std::max<int64_t>(1, std::min(slots, most)));
+    pl->split_target = pl->grid_x;
+    if (fp4_warp_workers(s, opt, pl->row_chunks, pl->rows_per_cta))
+      pl->split_target *= pl->threads_per_cta / 32;
     pl->stream_k = 1;
     pl->split_blocks = 0;
     pl->num_splits = std::min(pl->split_target, max_blocks);
-    pl->grid_x = pl->split_target;
     pl->grid_y = pl->grid_z = 1;
     pl->ctas_per_sm = ctas_per_sm;
     pl->workspace_bytes = workspace_layout(s, pl->num_splits, pl->row_chunks, pl->rows_per_cta, 2,
@@ -435,7 +458,7 @@ void plan_splits(const Shape &s, const pkv_options *opt, int num_sms, int ctas_p
   pl->merge_kernel = 0;
   if (num_splits > 1) {
     const WorkspaceLayout w = workspace_layout(s, num_splits, pl->row_chunks, pl->rows_per_cta,
-                                               persistent ? 2 : (opt ? opt->merge : 0));
+                                               separate_merge ? 2 : (opt ? opt->merge : 0));
     pl->workspace_bytes = w.total;
     pl->merge_kernel = w.fused_merge ? 0 : 1;
   }
@@ -614,7 +637,9 @@ pkv_status run_attention(void *out, const void *q, const void *k_cache, const vo
   p.num_splits = pl.num_splits;
   p.split_target = pl.split_target;
   p.stream_k = pl.stream_k;
-  p.sk_weight = !pl.stream_k ? 0 : (s.dtype == PKV_FP4_E2M1 ? kFp4Weight : kStreamKWeight);
+  p.sk_weight = !pl.stream_k ? 0
+                : s.dtype != PKV_FP4_E2M1 ? kStreamKWeight
+                : pl.split_target > pl.grid_x ? kFp4WarpWeight : kFp4Weight;
   p.scale_log2 =
       static_cast<float>(static_cast<double>(scale) * 1.4426950408889634 * k_scale);
   p.out_scale = v_scale;
@@ -622,7 +647,9 @@ pkv_status run_attention(void *out, const void *q, const void *k_cache, const vo
   if (pl.num_splits > 1 || pl.split_target > 0) {
     const WorkspaceLayout w =
         workspace_layout(s, pl.num_splits, pl.row_chunks, pl.rows_per_cta,
-                         pl.kernel == PKV_KERNEL_TC ? 2 : (opt ? opt->merge : 0),
+                         pl.kernel == PKV_KERNEL_TC || s.dtype == PKV_FP4_E2M1
+                             ? 2
+                             : (opt ? opt->merge : 0),
                          pl.split_target, pl.stream_k);
     char *base = static_cast<char *>(workspace);
     p.part_o = reinterpret_cast<float *>(base);

@@ -116,9 +116,13 @@ cudaError_t simt_fp4_launch(pkv_dtype q_dtype, int head_dim, int rows, const Att
                             dim3 grid, cudaStream_t stream);
 
 // Tensor-core attention over a 4-bit cache (attn_fp4.cu): bf16 / f16 q, `tiles`
-// 8-column tiles of query rows per CTA.
+// 8-column tiles of query rows per worker.  Workers of the balanced partition
+// are CTAs, or (warp_workers, up to mma_fp4_max_warp_tiles; p.split_target is
+// then 4 times the grid) warps.
 int mma_fp4_max_tiles(int head_dim);
-bool mma_fp4_kernel_info(pkv_dtype q_dtype, int head_dim, int tiles, KernelInfo *info);
+int mma_fp4_max_warp_tiles(int head_dim);
+bool mma_fp4_kernel_info(pkv_dtype q_dtype, int head_dim, int tiles, bool warp_workers,
+                         KernelInfo *info);
 cudaError_t mma_fp4_launch(pkv_dtype q_dtype, int head_dim, int tiles, const AttnParams &p,
                            dim3 grid, cudaStream_t stream);
 

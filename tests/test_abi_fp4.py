@@ -69,7 +69,7 @@ def test_the_type_is_refused_by_the_plain_entry_points(L):
     assert L.pkv_copy_blocks(16, 16, 16, 16, 1, 4, 72, 16, 10, 4, None, None) == 2   # not a D
 
 
-@pytest.mark.parametrize("field", ["stages", "warp_tiles", "blocks_per_iter", "persistent"])
+@pytest.mark.parametrize("field", ["merge", "stages", "warp_tiles", "blocks_per_iter", "persistent"])
 def test_launch_controls_that_do_not_apply_are_refused(L, field):
     opt = binding.Options()
     setattr(opt, field, 1)

@@ -203,12 +203,12 @@ def test_attention(dtype, D, Q, Hq, Hkv):
 
 @pytest.mark.parametrize("kernel", [0, 1])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("split_blocks", [1, 3, 16])
-@pytest.mark.parametrize("merge", [1, 2])
-def test_splits_and_merges(kernel, dtype, split_blocks, merge):
-    run(W.Workload("fp4 split", 4, 32, 8, 128, dtype, context_lens=[1, 200, 1500, 3000],
-                   seed=2100 + split_blocks), kernel=kernel, split_blocks=split_blocks,
-        merge=merge)
+@pytest.mark.parametrize("split_blocks", [1, 3, 16, 1000])
+@pytest.mark.parametrize("Q", [1, 4])
+def test_splits(kernel, dtype, split_blocks, Q):
+    run(W.Workload("fp4 split", 4, 32, 8, 128, dtype, context_lens=[Q, 200, 1500, 3000],
+                   num_queries=Q, seed=2100 + split_blocks), kernel=kernel,
+        split_blocks=split_blocks)
 
 
 @pytest.mark.parametrize("kernel", [0, 1])
@@ -216,6 +216,20 @@ def test_splits_and_merges(kernel, dtype, split_blocks, merge):
 def test_row_chunks(kernel, rows):
     run(W.Workload("fp4 chunks", 3, 12, 2, 128, "f16", context_lens=[7, 64, 517], num_queries=4,
                    seed=2150), kernel=kernel, rows_per_cta=rows)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Q,Hq,Hkv,tiles,chunks", [(2, 8, 2, 1, 1), (3, 8, 2, 2, 1),
+                                                   (5, 8, 2, 3, 1), (8, 8, 2, 4, 1),
+                                                   (10, 8, 2, 5, 1), (11, 8, 2, 3, 2),
+                                                   (31, 4, 1, 4, 4)])
+@pytest.mark.parametrize("split_blocks", [0, 5])
+def test_every_column_tile(D, Q, Hq, Hkv, tiles, chunks, split_blocks):
+    lens = [Q, Q + 1, Q + 40, 333, 1200]
+    p = pkv.plan(len(lens), Q, Hq, Hkv, D, max(lens), "fp4", split_blocks=split_blocks)
+    assert (p["warp_tiles"], p["row_chunks"]) == (tiles, chunks)
+    run(W.Workload("fp4 tiles", len(lens), Hq, Hkv, D, "bf16", context_lens=lens, num_queries=Q,
+                   seed=2155 + Q), split_blocks=split_blocks)
 
 
 @pytest.mark.parametrize("kernel", [0, 1])
@@ -291,22 +305,38 @@ def test_bad_blocks_and_lengths_are_recorded(dtype):
     assert torch.equal(out, keep["out"])
 
 
-def test_a_nan_block_reaches_the_rows_that_see_it():
-    wl = W.Workload("fp4 nan", 2, 4, 2, 128, "bf16", context_lens=[20, 20], seed=2220)
+@pytest.mark.parametrize("L", [20, 3000])
+@pytest.mark.parametrize("dtype,kernel,split_blocks", [
+    ("bf16", 0, 0), ("bf16", 0, 16), ("bf16", 1, 0), ("f32", 0, 16), ("f32", 0, 0)])
+def test_a_nan_block_reaches_the_rows_that_see_it(L, dtype, kernel, split_blocks):
+    wl = W.Workload("fp4 nan", 2, 4, 2, 128, dtype, context_lens=[L, L], seed=2220)
     keep = {}
-    run(wl, keep=keep)
+    run(wl, keep=keep, kernel=kernel, split_blocks=split_blocks)
     b = keep["b"]
-    kn = dev_tensor(b.k_new, "bf16", DEV).clone()
-    vn = dev_tensor(b.v_new, "bf16", DEV)
+    kn = dev_tensor(b.k_new, dtype, DEV).clone()
+    vn = dev_tensor(b.v_new, dtype, DEV)
     kn[0, 1, 3] = float("nan")
     slots = torch.from_numpy(b.slot_mapping).to(DEV)
     pkv.kv_append_fp4(kn, vn, keep["dk"], keep["dv"], slots, K_SCALE, V_SCALE)
     out = pkv.paged_attention_fp4(keep["q"], keep["dk"], keep["dv"],
                                   torch.from_numpy(b.block_table).to(DEV),
                                   torch.from_numpy(b.context_lens).to(DEV), K_SCALE, V_SCALE,
-                                  scale=wl.softmax_scale, max_context_len=20)
+                                  scale=wl.softmax_scale, max_context_len=L, kernel=kernel,
+                                  split_blocks=split_blocks)
     assert torch.isnan(out[0, 2:].float()).all()              # heads of KV head 1
     assert torch.equal(out[0, :2], keep["out"][0, :2]) and torch.equal(out[1], keep["out"][1])
+
+
+@pytest.mark.parametrize("Q,lens", [(1, [0, 300, 5, 4000, 0, 16, 17, 1]), (1, [2000]),
+                                    (4, [4, 900, 35, 64])])
+@pytest.mark.parametrize("batch", [1, 40])
+def test_balanced_partition(Q, lens, batch):
+    # ragged and empty sequences, beyond 32 of them, workers CTAs or warps
+    wl = W.Workload("fp4 balanced", len(lens) * batch, 16, 16 if Q == 1 else 4, 64, "bf16",
+                    context_lens=lens * batch, num_queries=Q, seed=2225)
+    p = pkv.plan(wl.batch, Q, 16, wl.num_kv_heads, 64, max(lens), "fp4")
+    assert p["stream_k"] == 1 and p["split_target"] % p["grid_x"] == 0
+    run(wl)
 
 
 # ---- as a program uses it ---------------------------------------------------------------
