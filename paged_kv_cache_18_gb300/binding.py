@@ -8,9 +8,10 @@ been built, or a call fails, an exception is raised.
 """
 from __future__ import annotations
 
-import contextlib
+import array
 import ctypes
 import functools
+import operator
 import os
 import threading
 from typing import Optional
@@ -142,9 +143,8 @@ def lib() -> ctypes.CDLL:
             L.pkv_paged_attention_fp4.argtypes = [vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32,
                                                   i32, i32, i32, i64, f32, i32, f32, f32, vp, i64,
                                                   vp, sz, opt, vp, vp]
-            L.pkv_commit_rows.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(vp), i32, vp, i32, vp,
-                                          vp, i32, vp, i32, i32, i32, i32, i32, i64, i32, vp, vp,
-                                          vp]
+            L.pkv_commit_rows.argtypes = [vp, vp, i32, vp, i32, vp, vp, i32, vp, i32, i32, i32, i32,
+                                          i32, i64, i32, vp, vp, vp]
             L.pkv_paged_decode_attention_noalloc.argtypes = [vp, vp, vp, vp, vp, i32, vp, i32,
                                                              i32, i32, i32, i32, i32, i64, f32,
                                                              i32, opt, vp, vp]
@@ -680,37 +680,29 @@ def fp4_cache_shape(num_blocks: int, num_kv_heads: int, head_dim: int) -> tuple:
     return (num_blocks, num_kv_heads, 16, 9 * head_dim // 16)
 
 
-_NO_GUARD = contextlib.nullcontext()
-
-
-def _on_device(device_index: int):
-    """The library launches on the current device: make it the tensors' one."""
-    if torch.cuda.current_device() == device_index:
-        return _NO_GUARD
-    return torch.cuda.device(device_index)
-
-
-def _on_one_device(what: str, *tensors) -> int:
-    """The CUDA device index that all the tensors (None: absent) share."""
-    index = tensors[0].get_device()
-    _need(index >= 0 and all(t is None or t.get_device() == index for t in tensors),
-          f"{what} must be on one CUDA device")
-    return index
+# The calls below check their arguments inline: they are made once a layer and
+# step, and a helper call or a formatted message each costs as much as a check.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_ONE_DEVICE = "all tensors of a call must be on one CUDA device"
 
 
 def _fp4_cache_args(k_cache, v_cache):
-    _need(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and k_cache.dtype == torch.uint8
-          and v_cache.dtype == torch.uint8 and k_cache.is_contiguous() and v_cache.is_contiguous()
-          and k_cache.shape[2] == 16 and k_cache.shape[3] in (36, 72, 144),
-          "4-bit caches: contiguous uint8 [num_blocks, num_kv_heads, 16, 9 * head_dim / 16] "
-          "(fp4_cache_shape), head_dim 64, 128 or 256")
-    NB, Hkv, bs, row = k_cache.shape
-    return NB, Hkv, bs, row * 16 // 9
+    shape = k_cache.shape
+    if not (len(shape) == 4 and v_cache.shape == shape and k_cache.dtype is torch.uint8
+            and v_cache.dtype is torch.uint8 and k_cache.is_contiguous()
+            and v_cache.is_contiguous() and shape[2] == 16 and shape[3] in (36, 72, 144)):
+        raise ValueError("4-bit caches: contiguous uint8 [num_blocks, num_kv_heads, 16, "
+                         "9 * head_dim / 16] (fp4_cache_shape), head_dim 64, 128 or 256")
+    return shape[0], shape[1], shape[3] * 16 // 9
 
 
-def _slots_arg(slot_mapping, T):
-    _need(slot_mapping.dtype == torch.int64 and slot_mapping.shape == (T,)
-          and slot_mapping.is_contiguous(), "slot_mapping int64 [T]")
+def _error_arg(error_word, dev):
+    if error_word is None:
+        return None
+    if not (error_word.dtype is torch.int32 and error_word.get_device() == dev
+            and error_word.numel() >= 1):
+        raise ValueError("error_word must be an int32 tensor on the call's device")
+    return error_word.data_ptr()
 
 
 def kv_append_fp4(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor,
@@ -718,19 +710,30 @@ def kv_append_fp4(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tenso
                   v_scale: float, error_word: Optional[torch.Tensor] = None) -> None:
     """Quantise k_new/v_new [T, Hkv, D] (float32/bf16/f16) into the 4-bit
     caches (fp4_cache_shape) at their slots (pkv_kv_append_fp4)."""
-    NB, Hkv, bs, D = _fp4_cache_args(k_cache, v_cache)
-    T = k_new.shape[0]
-    _need(k_new.shape == (T, Hkv, D) and v_new.shape == (T, Hkv, D)
-          and k_new.dtype == v_new.dtype and k_new.dtype in _DTYPE
-          and k_new.is_contiguous() and v_new.is_contiguous(), "k_new/v_new [T, Hkv, D]")
-    _slots_arg(slot_mapping, T)
-    dev = _on_one_device("k_new, v_new, caches and slot_mapping", k_cache, v_cache, k_new, v_new,
-                         slot_mapping, error_word)
-    with _on_device(dev):
-        _check("pkv_kv_append_fp4", lib().pkv_kv_append_fp4(
-            k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            slot_mapping.data_ptr(), T, Hkv, D, bs, NB, _DTYPE[k_new.dtype], float(k_scale),
-            float(v_scale), _err_ptr(error_word), _stream(k_cache)))
+    NB, Hkv, D = _fp4_cache_args(k_cache, v_cache)
+    shape, dt = k_new.shape, _DTYPE.get(k_new.dtype)
+    if not (len(shape) == 3 and shape[1] == Hkv and shape[2] == D and v_new.shape == shape
+            and dt is not None and v_new.dtype is k_new.dtype and k_new.is_contiguous()
+            and v_new.is_contiguous()):
+        raise ValueError("k_new/v_new: contiguous [T, Hkv, D], float32, bfloat16 or float16")
+    T = shape[0]
+    if not (slot_mapping.dtype is torch.int64 and slot_mapping.shape == (T,)
+            and slot_mapping.is_contiguous()):
+        raise ValueError("slot_mapping int64 [T]")
+    dev = k_cache.get_device()
+    if not (dev >= 0 and v_cache.get_device() == dev and k_new.get_device() == dev
+            and v_new.get_device() == dev and slot_mapping.get_device() == dev):
+        raise ValueError(_ONE_DEVICE)
+    err = _error_arg(error_word, dev)
+    if dev != _current_device():  # the library launches on the current device
+        with torch.cuda.device(dev):
+            return kv_append_fp4(k_new, v_new, k_cache, v_cache, slot_mapping, k_scale, v_scale,
+                                 error_word)
+    st = lib().pkv_kv_append_fp4(
+        k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        slot_mapping.data_ptr(), T, Hkv, D, 16, NB, dt, k_scale, v_scale, err, _stream(k_cache))
+    if st:
+        _check("pkv_kv_append_fp4", st)
 
 
 def kv_load_fp4(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping: torch.Tensor,
@@ -740,35 +743,49 @@ def kv_load_fp4(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping: torc
     """The rows of slots ``slot_mapping`` [T] of the 4-bit caches as (k, v)
     [T, Hkv, D] of ``dtype``; padding (negative slots) reads as zeros
     (pkv_kv_load_fp4)."""
-    NB, Hkv, bs, D = _fp4_cache_args(k_cache, v_cache)
-    T = slot_mapping.shape[0]
-    _slots_arg(slot_mapping, T)
-    _need(dtype in _DTYPE, "dtype: float32, bfloat16 or float16")
+    NB, Hkv, D = _fp4_cache_args(k_cache, v_cache)
+    if not (slot_mapping.dtype is torch.int64 and slot_mapping.dim() == 1
+            and slot_mapping.is_contiguous()):
+        raise ValueError("slot_mapping int64 [T]")
+    dt = _DTYPE.get(dtype)
+    if dt is None:
+        raise ValueError("dtype: float32, bfloat16 or float16")
+    dev = k_cache.get_device()
+    if not (dev >= 0 and v_cache.get_device() == dev and slot_mapping.get_device() == dev):
+        raise ValueError(_ONE_DEVICE)
+    if dev != _current_device():  # the library launches on the current device
+        with torch.cuda.device(dev):
+            return kv_load_fp4(k_cache, v_cache, slot_mapping, k_scale, v_scale, dtype, k_out,
+                               v_out, error_word)
+    shape = (slot_mapping.shape[0], Hkv, D)
     if k_out is None:
-        k_out = torch.empty(T, Hkv, D, dtype=dtype, device=k_cache.device)
+        k_out = torch.empty(shape, dtype=dtype, device=k_cache.device)
+    elif not (k_out.shape == shape and k_out.dtype is dtype and k_out.is_contiguous()):
+        raise ValueError("k_out: contiguous [T, Hkv, D] of dtype")
     if v_out is None:
-        v_out = torch.empty(T, Hkv, D, dtype=dtype, device=k_cache.device)
-    for t in (k_out, v_out):
-        _need(t.shape == (T, Hkv, D) and t.dtype == dtype and t.is_contiguous(),
-              "k_out / v_out: contiguous [T, Hkv, D] of dtype")
-    dev = _on_one_device("caches, slot_mapping and outputs", k_cache, v_cache, slot_mapping,
-                         k_out, v_out, error_word)
-    with _on_device(dev):
-        _check("pkv_kv_load_fp4", lib().pkv_kv_load_fp4(
-            k_out.data_ptr(), v_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            slot_mapping.data_ptr(), T, Hkv, D, bs, NB, _DTYPE[dtype], float(k_scale),
-            float(v_scale), _err_ptr(error_word), _stream(k_cache)))
+        v_out = torch.empty_like(k_out)
+    elif not (v_out.shape == shape and v_out.dtype is dtype and v_out.is_contiguous()):
+        raise ValueError("v_out: contiguous [T, Hkv, D] of dtype")
+    if k_out.get_device() != dev or v_out.get_device() != dev:
+        raise ValueError(_ONE_DEVICE)
+    st = lib().pkv_kv_load_fp4(
+        k_out.data_ptr(), v_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        slot_mapping.data_ptr(), shape[0], Hkv, D, 16, NB, dt, k_scale, v_scale,
+        _error_arg(error_word, dev), _stream(k_cache))
+    if st:
+        _check("pkv_kv_load_fp4", st)
     return k_out, v_out
 
 
 @functools.lru_cache(maxsize=1024)
-def _fp4_workspace(device_index: int, B: int, Q: int, Hq: int, Hkv: int, D: int, bs: int,
-                   max_context_len: int, options: tuple) -> int:
-    """Workspace bytes of a call on the current device (a function of sizes)."""
+def _fp4_workspace(dev: int, B: int, Q: int, Hq: int, Hkv: int, D: int, max_context_len: int,
+                   options: Optional[tuple]) -> int:
+    """Workspace bytes of a call on device ``dev``, the current one (a function
+    of the sizes)."""
     n = ctypes.c_size_t(0)
     _check("pkv_attention_workspace_size", lib().pkv_attention_workspace_size(
-        B, Q, Hq, Hkv, D, bs, max_context_len, PKV_FP4_E2M1,
-        ctypes.byref(Options(*options)) if any(options) else None, ctypes.byref(n)))
+        B, Q, Hq, Hkv, D, 16, max_context_len, PKV_FP4_E2M1,
+        ctypes.byref(Options(*options)) if options else None, ctypes.byref(n)))
     return int(n.value)
 
 
@@ -785,51 +802,76 @@ def paged_attention_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     ``tree_mask`` (int64 [Q] or [B, Q], as for tree_verify_attention), tree
     verification over 4-bit caches (pkv_paged_attention_fp4); out has q's shape
     and type."""
-    NB, Hkv, bs, D = _fp4_cache_args(k_cache, v_cache)
-    _need(q.dim() in (3, 4) and q.is_contiguous() and q.dtype in _DTYPE and q.shape[-1] == D,
-          "q must be a contiguous [B, Hq, D] or [B, Q, Hq, D]")
-    B, Hq = q.shape[0], q.shape[-2]
-    Q = q.shape[1] if q.dim() == 4 else 1
-    _need(block_table.dtype == torch.int32 and block_table.dim() == 2
-          and block_table.shape[0] == B and block_table.is_contiguous(),
-          "block_table must be a contiguous int32 [batch, max_blocks_per_seq]")
-    _need(context_lens.dtype == torch.int32 and context_lens.shape == (B,)
-          and context_lens.is_contiguous(), "context_lens must be a contiguous int32 [batch]")
-    stride = 0
+    NB, Hkv, D = _fp4_cache_args(k_cache, v_cache)
+    shape, dt = q.shape, _DTYPE.get(q.dtype)
+    if len(shape) == 3:
+        B, Hq, Dq = shape
+        Q = 1
+    elif len(shape) == 4:
+        B, Q, Hq, Dq = shape
+    else:
+        Dq = None
+    if Dq != D or dt is None or not q.is_contiguous():
+        raise ValueError("q must be a contiguous [B, Hq, D] or [B, Q, Hq, D]")
+    if not (block_table.dtype is torch.int32 and block_table.dim() == 2
+            and block_table.shape[0] == B and block_table.is_contiguous()):
+        raise ValueError("block_table must be a contiguous int32 [batch, max_blocks_per_seq]")
+    if not (context_lens.dtype is torch.int32 and context_lens.shape == (B,)
+            and context_lens.is_contiguous()):
+        raise ValueError("context_lens must be a contiguous int32 [batch]")
+    dev = q.get_device()
+    mask, stride, mask_dev = None, 0, dev
     if tree_mask is not None:
-        _need(tree_mask.dtype == torch.int64 and tree_mask.is_contiguous()
-              and tree_mask.shape in ((Q,), (B, Q)), "tree_mask: int64 [Q] or [B, Q]")
-        stride = 0 if tree_mask.dim() == 1 else Q
+        if not (tree_mask.dtype is torch.int64 and tree_mask.is_contiguous()
+                and tree_mask.shape in ((Q,), (B, Q))):
+            raise ValueError("tree_mask: int64 [Q] or [B, Q]")
+        mask, stride = tree_mask.data_ptr(), 0 if tree_mask.dim() == 1 else Q
+        mask_dev = tree_mask.get_device()
+    if not (dev >= 0 and k_cache.get_device() == dev and v_cache.get_device() == dev
+            and block_table.get_device() == dev and context_lens.get_device() == dev
+            and mask_dev == dev):
+        raise ValueError(_ONE_DEVICE)
+    if dev != _current_device():  # the library launches on the current device
+        with torch.cuda.device(dev):
+            return paged_attention_fp4(q, k_cache, v_cache, block_table, context_lens, k_scale,
+                                       v_scale, scale, max_context_len, tree_mask, out,
+                                       workspace, kernel, split_blocks, error_word)
     if out is None:
         out = torch.empty_like(q)
-    _need(out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous(), "out")
-    dev = _on_one_device("q, caches, block_table, context_lens, tree_mask, out and workspace", q,
-                         k_cache, v_cache, block_table, context_lens, out, tree_mask, workspace,
-                         error_word)
+    elif not (out.shape == shape and out.dtype is q.dtype and out.is_contiguous()
+              and out.get_device() == dev):
+        raise ValueError("out must be contiguous, of q's shape, type and device")
     if max_context_len is None:
         max_context_len = int(context_lens.max().item()) if B else 0  # device read
-    options = (kernel, split_blocks, 0, TUNING.get("rows_per_cta", 0), TUNING.get("merge", 0), 0, 0,
-               0, TUNING.get("split_waves", 0))
-    with _on_device(dev):
-        if workspace is None:
-            need = _fp4_workspace(dev, B, Q, Hq, Hkv, D, bs, max_context_len, options)
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        _need(workspace is None or workspace.is_contiguous(), "workspace must be contiguous")
-        _check("pkv_paged_attention_fp4", lib().pkv_paged_attention_fp4(
-            out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            block_table.data_ptr(), block_table.shape[1], context_lens.data_ptr(),
-            max_context_len, B, Q, Hq, Hkv, D, bs, NB, 0.0 if scale is None else float(scale),
-            _DTYPE[q.dtype], float(k_scale), float(v_scale),
-            None if tree_mask is None else tree_mask.data_ptr(), stride,
-            None if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.numel() * workspace.element_size(),
-            ctypes.byref(Options(*options)) if any(options) else None, _err_ptr(error_word),
-            _stream(q)))
+    options = None
+    if kernel or split_blocks or TUNING:
+        options = (kernel, split_blocks, 0, TUNING.get("rows_per_cta", 0),
+                   TUNING.get("merge", 0), 0, 0, 0, TUNING.get("split_waves", 0))
+    ws, ws_bytes = None, 0
+    if workspace is None:
+        ws_bytes = _fp4_workspace(dev, B, Q, Hq, Hkv, D, max_context_len, options)
+        if ws_bytes:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+            ws = workspace.data_ptr()
+    else:
+        if not workspace.is_contiguous() or workspace.get_device() != dev:
+            raise ValueError("workspace must be contiguous, on the call's device")
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    st = lib().pkv_paged_attention_fp4(
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        block_table.data_ptr(), block_table.shape[1], context_lens.data_ptr(), max_context_len, B,
+        Q, Hq, Hkv, D, 16, NB, 0.0 if scale is None else scale, dt, k_scale, v_scale, mask, stride,
+        ws, ws_bytes, ctypes.byref(Options(*options)) if options else None,
+        _error_arg(error_word, dev), _stream(q))
+    if st:
+        _check("pkv_paged_attention_fp4", st)
     return out
 
 
 # ---- the accepted path of a verified tree ------------------------------------------
+_SHAPE, _TYPE = operator.attrgetter("shape"), operator.attrgetter("dtype")
+
+
 def commit_rows(k_caches, v_caches, block_table: torch.Tensor, context_lens: torch.Tensor,
                 path: torch.Tensor, path_lens: torch.Tensor, num_queries: int, fp4: bool = False,
                 new_lens: Optional[torch.Tensor] = None,
@@ -842,49 +884,67 @@ def commit_rows(k_caches, v_caches, block_table: torch.Tensor, context_lens: tor
     k_caches, v_caches: lists of equally shaped caches, one per layer, [NB, Hkv,
     16, D] (uint8: FP8 codes, or with ``fp4`` 4-bit caches of fp4_cache_shape);
     MLA latents [NB, 16, W]: v_caches None.  path: int32 [B, max_path]."""
-    caches = list(k_caches) + (list(v_caches) if v_caches is not None else [])
     n = len(k_caches)
-    _need(n >= 1 and len(caches) == (n if v_caches is None else 2 * n),
-          "k_caches / v_caches: one tensor per layer")
+    if n < 1 or (v_caches is not None and len(v_caches) != n):
+        raise ValueError("k_caches / v_caches: one tensor per layer")
+    caches = [*k_caches, *v_caches] if v_caches is not None else list(k_caches)
     first = caches[0]
-    _need(first.dim() == 4 or (first.dim() == 3 and v_caches is None),
-          "caches: [NB, Hkv, 16, D], or latents [NB, 16, W] without v_caches")
-    shape, dtype = first.shape, first.dtype
-    _need(all(t.shape == shape and t.dtype == dtype and t.is_contiguous() for t in caches),
-          "caches must be contiguous and of one shape and dtype")
+    shape = first.shape
+    if not (len(shape) == 4 or (len(shape) == 3 and v_caches is None)):
+        raise ValueError("caches: [NB, Hkv, 16, D], or latents [NB, 16, W] without v_caches")
+    # (two tensors times the layers: checked without a loop in Python, which costs more
+    # than the kernel)
+    count = len(caches)
+    if not (list(map(_SHAPE, caches)).count(shape) == count
+            and list(map(_TYPE, caches)).count(first.dtype) == count
+            and all(map(torch.Tensor.is_contiguous, caches))):
+        raise ValueError("caches must be contiguous and of one shape and dtype")
     if fp4:
-        _need(v_caches is not None, "4-bit caches come as keys and values")
-        NB, Hkv, bs, D = _fp4_cache_args(first, first)
-        dt = PKV_FP4_E2M1
+        if v_caches is None:
+            raise ValueError("4-bit caches come as keys and values")
+        NB, Hkv, D = _fp4_cache_args(first, first)
+        bs, dt = 16, PKV_FP4_E2M1
     else:
-        _need(dtype in _DTYPE or dtype == torch.uint8, "cache dtype")
+        dt = PKV_FP8_E4M3 if first.dtype is torch.uint8 else _DTYPE.get(first.dtype)
+        if dt is None:
+            raise ValueError("cache dtype")
         NB, bs, D = shape[0], shape[-2], shape[-1]
-        Hkv = shape[1] if first.dim() == 4 else 1
-        dt = PKV_FP8_E4M3 if dtype == torch.uint8 else _DTYPE[dtype]
-    B = context_lens.shape[0]
-    _need(block_table.dtype == torch.int32 and block_table.dim() == 2
-          and block_table.shape[0] == B and block_table.is_contiguous(),
-          "block_table must be a contiguous int32 [batch, max_blocks_per_seq]")
-    _need(context_lens.dtype == torch.int32 and context_lens.dim() == 1
-          and context_lens.is_contiguous(), "context_lens must be a contiguous int32 [batch]")
-    _need(path.dtype == torch.int32 and path.dim() == 2 and path.shape[0] == B
-          and path.is_contiguous(), "path must be a contiguous int32 [batch, max_path]")
-    _need(path_lens.dtype == torch.int32 and path_lens.shape == (B,)
-          and path_lens.is_contiguous(), "path_lens must be a contiguous int32 [batch]")
+        Hkv = shape[1] if len(shape) == 4 else 1
+    B = context_lens.shape[0] if context_lens.dim() == 1 else -1
+    if not (context_lens.dtype is torch.int32 and B >= 0 and context_lens.is_contiguous()):
+        raise ValueError("context_lens must be a contiguous int32 [batch]")
+    if not (block_table.dtype is torch.int32 and block_table.dim() == 2
+            and block_table.shape[0] == B and block_table.is_contiguous()):
+        raise ValueError("block_table must be a contiguous int32 [batch, max_blocks_per_seq]")
+    if not (path.dtype is torch.int32 and path.dim() == 2 and path.shape[0] == B
+            and path.is_contiguous()):
+        raise ValueError("path must be a contiguous int32 [batch, max_path]")
+    if not (path_lens.dtype is torch.int32 and path_lens.shape == (B,)
+            and path_lens.is_contiguous()):
+        raise ValueError("path_lens must be a contiguous int32 [batch]")
+    dev = first.get_device()
+    if not (dev >= 0 and list(map(torch.Tensor.get_device, caches)).count(dev) == count
+            and block_table.get_device() == dev and context_lens.get_device() == dev
+            and path.get_device() == dev and path_lens.get_device() == dev):
+        raise ValueError(_ONE_DEVICE)
+    if dev != _current_device():  # the library launches on the current device
+        with torch.cuda.device(dev):
+            return commit_rows(k_caches, v_caches, block_table, context_lens, path, path_lens,
+                               num_queries, fp4, new_lens, error_word)
     if new_lens is None:
         new_lens = torch.empty_like(context_lens)
-    _need(new_lens.dtype == torch.int32 and new_lens.shape == (B,) and new_lens.is_contiguous(),
-          "new_lens must be a contiguous int32 [batch]")
-    dev = _on_one_device("caches, block_table, lengths and paths", block_table, context_lens,
-                         path, path_lens, new_lens, error_word, *caches)
-    ptrs = [t.data_ptr() for t in caches]
-    array = ctypes.c_void_p * n
-    with _on_device(dev):
-        _check("pkv_commit_rows", lib().pkv_commit_rows(
-            array(*ptrs[:n]), array(*ptrs[n:]) if v_caches is not None else None, n,
-            block_table.data_ptr(), block_table.shape[1], context_lens.data_ptr(),
-            path.data_ptr(), path.shape[1], path_lens.data_ptr(), B, int(num_queries), Hkv, D, bs,
-            NB, dt, new_lens.data_ptr(), _err_ptr(error_word), _stream(block_table)))
+    elif not (new_lens.dtype is torch.int32 and new_lens.shape == (B,)
+              and new_lens.is_contiguous() and new_lens.get_device() == dev):
+        raise ValueError("new_lens must be a contiguous int32 [batch]")
+    ptrs = array.array("Q", map(torch.Tensor.data_ptr, caches))
+    k_ptrs = ptrs.buffer_info()[0]
+    v_ptrs = None if v_caches is None else k_ptrs + 8 * n
+    st = lib().pkv_commit_rows(
+        k_ptrs, v_ptrs, n, block_table.data_ptr(), block_table.shape[1], context_lens.data_ptr(),
+        path.data_ptr(), path.shape[1], path_lens.data_ptr(), B, num_queries, Hkv, D, bs, NB, dt,
+        new_lens.data_ptr(), _error_arg(error_word, dev), _stream(first))
+    if st:
+        _check("pkv_commit_rows", st)
     return new_lens
 
 

@@ -9,13 +9,21 @@
 // zeros or NaN.  Load: out = (code * s) t, the product in brackets exact, one
 // rounding to float32 and one to the output type.
 //
-// One thread takes one scale block of one (token, KV head): 16 elements on one
-// side, 8 code bytes and a scale byte on the other; keys and values are
-// separate halves of the grid.  Threads run over a row's blocks first for keys
-// (the row's code bytes are contiguous), and over 4 blocks of 8 consecutive
-// tokens for values, so that the 4-byte pieces of consecutive rows fill whole
-// 32-byte sectors of the tile while each token's elements are still taken 128
-// bytes (16-bit) at a time.  Bound by memory: 2.56 bytes an element at 16 bits.
+// One thread takes two scale blocks (32 dims) of one (token, KV head): 64 bytes
+// of 16-bit elements on one side, in whole 32-byte sectors, 16 code bytes and
+// two scale bytes on the other.  Keys and values are the two rows of the grid.
+// Threads run over a row's dims first for keys (a row's codes are contiguous),
+// and over 8 consecutive tokens first for values, whose rows lie 4 bytes apart
+// in the tile: 8 of them fill a sector.
+//
+// Bound by memory, 2.56 bytes an element at 16 bits, when the arithmetic stays
+// short: an IEEE division for every element, and 64-bit index divisions, took
+// three times as long as the bytes.  Quotients are therefore corrected products
+// with a correctly rounded reciprocal (Markstein 1990): for r = RN(1 / f) and
+// q = RN(x r), RN(q + r RN(x - q f)) is RN(x / f) unless f's significand is all
+// ones or something leaves the range; those cases divide.
+#include <algorithm>
+
 #include "fp4.cuh"
 #include "pkv_internal.h"
 
@@ -23,224 +31,257 @@ namespace pkv {
 namespace fp4 {
 namespace {
 
-template <typename T> struct Vec16;  // 16 elements in 16-byte vectors
-template <> struct Vec16<float> { static constexpr int n = 4; };
-template <> struct Vec16<__nv_bfloat16> { static constexpr int n = 2; };
-template <> struct Vec16<__half> { static constexpr int n = 2; };
-
-template <typename T>
-__device__ __forceinline__ void load16(const T *src, float (&x)[16]) {
-  uint4 w[Vec16<T>::n];
-#pragma unroll
-  for (int i = 0; i < Vec16<T>::n; ++i) w[i] = __ldg(reinterpret_cast<const uint4 *>(src) + i);
-  if constexpr (Vec16<T>::n == 4) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(reinterpret_cast<const uint32_t *>(w)[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      unpack2<T>(reinterpret_cast<const uint32_t *>(w)[i], x[2 * i], x[2 * i + 1]);
-  }
-}
-
-__device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) {
-  return Mma<__nv_bfloat16>::pack(a, b);
-}
-__device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
-  return Mma<__half>::pack(a, b);
-}
-
-template <typename T>
-__device__ __forceinline__ void store16(T *dst, const float (&x)[16]) {
-  uint32_t w[4 * Vec16<T>::n];
-  if constexpr (Vec16<T>::n == 4) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(x[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = pack2(x[2 * i], x[2 * i + 1], T{});
-  }
-#pragma unroll
-  for (int i = 0; i < Vec16<T>::n; ++i)
-    reinterpret_cast<uint4 *>(dst)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2],
-                                                   w[4 * i + 3]);
-}
-
-// The work of one thread: which scale block of which row.
-struct Item {
-  bool values;   // of the value cache, else of the key cache
-  int64_t token;
-  int head, blk;
-};
-template <int D>
-__device__ __forceinline__ Item item_of(int64_t i, int64_t tokens8, int heads) {
-  constexpr int S = Tile<D>::kScales;  // 4, 8 or 16
-  const int64_t half = tokens8 * heads * S;
-  Item it;
-  it.values = i >= half;
-  if (!it.values) {
-    it.blk = static_cast<int>(i % S);
-    const int64_t r = i / S;
-    it.head = static_cast<int>(r % heads);
-    it.token = r / heads;
-  } else {
-    i -= half;
-    const int low = static_cast<int>(i & 7), b4 = static_cast<int>((i >> 3) & 3);
-    int64_t r = i >> 5;
-    it.blk = static_cast<int>(r % (S / 4)) * 4 + b4;
-    r /= S / 4;
-    it.head = static_cast<int>(r % heads);
-    it.token = (r / heads) * 8 + low;
-  }
-  return it;
-}
-
-template <typename T, int D>
-__global__ void __launch_bounds__(256)
-    append_kernel(const T *__restrict__ k_new, const T *__restrict__ v_new,
-                  uint8_t *__restrict__ k_cache, uint8_t *__restrict__ v_cache,
-                  const int64_t *__restrict__ slots, int64_t num_tokens, int heads,
-                  int64_t num_blocks, float k_scale, float v_scale, int32_t *err) {
-  pdl_launch_dependents();  // as in kv_append_kernel
-  using TL = Tile<D>;
-  const int64_t tokens8 = (num_tokens + 7) / 8 * 8;
-  const int64_t total = 2 * tokens8 * heads * TL::kScales;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const Item it = item_of<D>(i, tokens8, heads);
-    if (it.token >= num_tokens) continue;
-    const int64_t slot = __ldg(slots + it.token);
-    if (slot < 0) continue;
-    if (slot >= num_blocks * kBlockSize) {
-      if (it.head == 0 && it.blk == 0) record_error(err, PKV_DEVERR_SLOT);
-      continue;
-    }
-    float x[16];
-    load16<T>((it.values ? v_new : k_new) + (it.token * heads + it.head) * D + it.blk * 16, x);
-    // largest magnitude, by the bit patterns: a NaN is larger than anything
-    uint32_t top = 0;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
-    const float t = it.values ? v_scale : k_scale;
-    const float ideal = __fdiv_rn(__fdiv_rn(__uint_as_float(top), t), 6.f);
-    const uint32_t sbyte = __nv_cvt_float_to_fp8(ideal, __NV_SATFINITE, __NV_E4M3) & 0x7fu;
-    const float f = __fmul_rn(e4m3_to_float(sbyte), t);
-    float y[2][8];
-    const bool live = f > 0.f;  // neither 0 nor NaN
-#pragma unroll
-    for (int e = 0; e < 16; ++e) y[e >> 3][e & 7] = live ? __fdiv_rn(x[e], f) : 0.f;
-    const uint32_t w0 = f32x8_to_e2m1(y[0]), w1 = f32x8_to_e2m1(y[1]);
-    const int row = static_cast<int>(slot % kBlockSize);
-    const int64_t tile = (slot / kBlockSize * heads + it.head) * TL::kBytes;
-    if (it.values) {
-      uint8_t *dst = v_cache + tile;
-      *reinterpret_cast<uint32_t *>(dst + TL::v_code(row, it.blk * 16)) = w0;
-      *reinterpret_cast<uint32_t *>(dst + TL::v_code(row, it.blk * 16 + 8)) = w1;
-      dst[TL::v_scale(row, it.blk)] = static_cast<uint8_t>(sbyte);
-    } else {
-      uint8_t *dst = k_cache + tile;
-      *reinterpret_cast<uint2 *>(dst + TL::k_code(row, it.blk * 16)) = make_uint2(w0, w1);
-      dst[TL::k_scale(row, it.blk)] = static_cast<uint8_t>(sbyte);
-    }
-  }
-}
-
-template <typename T, int D>
-__global__ void __launch_bounds__(256)
-    load_kernel(T *__restrict__ k_out, T *__restrict__ v_out, const uint8_t *__restrict__ k_cache,
-                const uint8_t *__restrict__ v_cache, const int64_t *__restrict__ slots,
-                int64_t num_tokens, int heads, int64_t num_blocks, float k_scale, float v_scale,
-                int32_t *err) {
-  using TL = Tile<D>;
-  const int64_t tokens8 = (num_tokens + 7) / 8 * 8;
-  const int64_t total = 2 * tokens8 * heads * TL::kScales;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const Item it = item_of<D>(i, tokens8, heads);
-    if (it.token >= num_tokens) continue;
-    const int64_t slot = __ldg(slots + it.token);
-    float x[16];
-    if (slot >= 0 && slot < num_blocks * kBlockSize) {
-      const int row = static_cast<int>(slot % kBlockSize);
-      const int64_t tile = (slot / kBlockSize * heads + it.head) * TL::kBytes;
-      uint32_t w0, w1, sbyte;
-      if (it.values) {
-        const uint8_t *src = v_cache + tile;
-        w0 = *reinterpret_cast<const uint32_t *>(src + TL::v_code(row, it.blk * 16));
-        w1 = *reinterpret_cast<const uint32_t *>(src + TL::v_code(row, it.blk * 16 + 8));
-        sbyte = src[TL::v_scale(row, it.blk)];
-      } else {
-        const uint8_t *src = k_cache + tile;
-        const uint2 w = *reinterpret_cast<const uint2 *>(src + TL::k_code(row, it.blk * 16));
-        w0 = w.x;
-        w1 = w.y;
-        sbyte = src[TL::k_scale(row, it.blk)];
-      }
-      const float s = e4m3_to_float(sbyte);
-      e2m1x8_to_float(w0, s, x);
-      e2m1x8_to_float(w1, s, x + 8);
-      const float t = it.values ? v_scale : k_scale;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] *= t;
-    } else {  // padding (slot < 0) and slots past the cache read as zeros
-      if (slot >= 0 && it.head == 0 && it.blk == 0) record_error(err, PKV_DEVERR_SLOT);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = 0.f;
-    }
-    store16<T>((it.values ? v_out : k_out) + (it.token * heads + it.head) * D + it.blk * 16, x);
-  }
-}
-
 struct RowArgs {
-  const void *k_new, *v_new;
-  void *k_out, *v_out;
-  void *k_cache, *v_cache;
+  const void *k_rows, *v_rows;  // new rows, or rows to fill
+  uint8_t *k_cache, *v_cache;
   const int64_t *slots;
-  int64_t num_tokens, num_blocks;
-  int heads;
-  float k_scale, v_scale;
+  int64_t num_blocks;
+  int num_tokens, heads;
+  float k_scale, v_scale, k_inv, v_inv;  // tensor scales and their reciprocals
+  int wide;                              // the rows are 32-byte aligned
   int32_t *err;
 };
 
-template <typename T, int D>
-cudaError_t rows_t(bool append, const RowArgs &a, int sm_count, cudaStream_t stream) {
-  const int64_t total = 2 * ((a.num_tokens + 7) / 8 * 8) * a.heads * Tile<D>::kScales;
-  int64_t ctas = (total + 255) / 256;
-  const int64_t cap = static_cast<int64_t>(sm_count) * 8;
-  if (ctas > cap) ctas = cap;
-  if (append) {
-    append_kernel<T, D><<<static_cast<unsigned>(ctas), 256, 0, stream>>>(
-        static_cast<const T *>(a.k_new), static_cast<const T *>(a.v_new),
-        static_cast<uint8_t *>(a.k_cache), static_cast<uint8_t *>(a.v_cache), a.slots,
-        a.num_tokens, a.heads, a.num_blocks, a.k_scale, a.v_scale, a.err);
+// 32 bytes of a row.
+__device__ __forceinline__ void load32(const void *src, int wide, uint32_t *w) {
+  if (wide) {
+    asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                   "=r"(w[6]), "=r"(w[7])
+                 : "l"(src));
   } else {
-    load_kernel<T, D><<<static_cast<unsigned>(ctas), 256, 0, stream>>>(
-        static_cast<T *>(a.k_out), static_cast<T *>(a.v_out),
-        static_cast<const uint8_t *>(a.k_cache), static_cast<const uint8_t *>(a.v_cache), a.slots,
-        a.num_tokens, a.heads, a.num_blocks, a.k_scale, a.v_scale, a.err);
+    const uint4 a = __ldg(static_cast<const uint4 *>(src));
+    const uint4 b = __ldg(static_cast<const uint4 *>(src) + 1);
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
   }
-  return cudaGetLastError();
+}
+__device__ __forceinline__ void store32(void *dst, int wide, const uint32_t *w) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    static_cast<uint4 *>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4 *>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
 
+// Whether the quotients by d may be corrected products.
+__host__ __device__ __forceinline__ bool plain_divisor(float d) {
+#ifdef __CUDA_ARCH__
+  const uint32_t bits = __float_as_uint(d);
+#else
+  union { float f; uint32_t u; } x;
+  x.f = d;
+  const uint32_t bits = x.u;
+#endif
+  // 2^-40 <= d < 2^40, significand not all ones
+  return (bits >> 23) - 87u < 80u && (bits & 0x7fffffu) != 0x7fffffu;
+}
+__device__ __forceinline__ float quotient(float x, float d, float inv) {
+  const float q = __fmul_rn(x, inv);
+  return __fmaf_rn(__fmaf_rn(-q, d, x), inv, q);
+}
+
+// Scale byte and codes of one block: w holds its 16 elements (8 or 16 words).
 template <typename T>
-cudaError_t rows_d(bool append, int D, const RowArgs &a, int sm_count, cudaStream_t stream) {
+__device__ __forceinline__ uint32_t encode16(const uint32_t *w, float t, float t_inv,
+                                             uint32_t (&codes)[2]) {
+  // largest magnitude, by the bit patterns: a NaN is larger than anything
+  float top;
+  if constexpr (Elt<T>::bytes == 4) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = max(m, w[i] & 0x7fffffffu);
+    top = __uint_as_float(m);
+  } else {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+    float a, b;
+    unpack2<T>(max(m & 0xffffu, m >> 16), a, b);
+    top = a;
+  }
+  const bool plain_top =
+      plain_divisor(t) && (top == 0.f || (__float_as_uint(top) >> 23) - 87u < 80u);
+  const float ideal = plain_top ? quotient(quotient(top, t, t_inv), 6.f, 1.f / 6.f)
+                                : __fdiv_rn(__fdiv_rn(top, t), 6.f);
+  const uint32_t sbyte = __nv_cvt_float_to_fp8(ideal, __NV_SATFINITE, __NV_E4M3) & 0x7fu;
+  const float f = __fmul_rn(e4m3_to_float(sbyte), t);
+  const bool live = f > 0.f;  // neither 0 nor NaN
+  // a normal scale below the largest: |x / f| < 6.5
+  const bool plain = plain_top && sbyte - 8u < 118u && plain_divisor(f);
+  const float inv = __frcp_rn(f);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float x[8], y[8];
+    if constexpr (Elt<T>::bytes == 4) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[8 * h + i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) unpack2<T>(w[4 * h + i], x[2 * i], x[2 * i + 1]);
+    }
+    if (plain) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = copysignf(quotient(x[i], f, inv), x[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = live ? __fdiv_rn(x[i], f) : 0.f;
+    }
+    codes[h] = f32x8_to_e2m1(y);
+  }
+  return sbyte;
+}
+
+// The 16 elements of a block (8 or 16 words) from its codes and scale byte.
+template <typename T>
+__device__ __forceinline__ void decode16(const uint32_t (&codes)[2], uint32_t sbyte, float t,
+                                         uint32_t *w) {
+  const float s = e4m3_to_float(sbyte);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float x[8];
+    e2m1x8_to_float(codes[h], s, x);  // exact
+    if constexpr (Elt<T>::bytes == 4) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[8 * h + i] = __float_as_uint(x[i] * t);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[4 * h + i] = Mma<T>::pack(x[2 * i] * t, x[2 * i + 1] * t);
+    }
+  }
+}
+
+template <typename T, int D, bool APPEND>
+__global__ void __launch_bounds__(256) rows_kernel(const RowArgs a) {
+  if (APPEND) pdl_launch_dependents();  // as in kv_append_kernel
+  using TL = Tile<D>;
+  constexpr int P = D / 32;                   // threads of a row
+  constexpr int WORDS = 8 * Elt<T>::bytes;    // words of 32 elements
+  const bool values = blockIdx.y != 0;
+  const unsigned per8 = 8u * P * a.heads;     // threads of 8 tokens
+  const unsigned i = blockIdx.x * 256u + threadIdx.x;
+  const unsigned chunk = i / per8, r = i - chunk * per8;
+  const int head = r / (8 * P);
+  const int pr = values ? (r >> 3) % P : r % P;
+  const int token = static_cast<int>(chunk * 8 + (values ? r & 7 : r / P & 7));
+  if (token >= a.num_tokens) return;
+  const int64_t slot = __ldg(a.slots + token);
+  T *row = static_cast<T *>(const_cast<void *>(values ? a.v_rows : a.k_rows)) +
+           (static_cast<int64_t>(token) * a.heads + head) * D + pr * 32;
+  const bool inside = slot >= 0 && slot < a.num_blocks * kBlockSize;
+  uint32_t w[WORDS];
+  if (APPEND) {  // (in flight together with the slot)
+#pragma unroll
+    for (int k = 0; k < WORDS / 8; ++k)
+      load32(reinterpret_cast<const char *>(row) + 32 * k, a.wide, w + 8 * k);
+  }
+  if (slot >= 0 && !inside && head == 0 && pr == 0 && !values)
+    record_error(a.err, PKV_DEVERR_SLOT);
+  const int at = static_cast<int>(slot % kBlockSize);
+  uint8_t *tile = (values ? a.v_cache : a.k_cache) +
+                  (slot / kBlockSize * a.heads + head) * static_cast<int64_t>(TL::kBytes);
+  const float t = values ? a.v_scale : a.k_scale;
+  uint32_t codes[2][2];
+  if (APPEND) {
+    if (!inside) return;
+    const float t_inv = values ? a.v_inv : a.k_inv;
+    const uint32_t s0 = encode16<T>(w, t, t_inv, codes[0]);
+    const uint32_t s1 = encode16<T>(w + WORDS / 2, t, t_inv, codes[1]);
+    if (values) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<uint32_t *>(tile + TL::v_code(at, pr * 32 + 8 * k)) =
+            codes[k >> 1][k & 1];
+      tile[TL::v_scale(at, 2 * pr)] = static_cast<uint8_t>(s0);
+      tile[TL::v_scale(at, 2 * pr + 1)] = static_cast<uint8_t>(s1);
+    } else {
+      *reinterpret_cast<uint4 *>(tile + TL::k_code(at, pr * 32)) =
+          make_uint4(codes[0][0], codes[0][1], codes[1][0], codes[1][1]);
+      *reinterpret_cast<uint16_t *>(tile + TL::k_scale(at, 2 * pr)) =
+          static_cast<uint16_t>(s0 | s1 << 8);
+    }
+  } else {
+    if (inside) {
+      uint32_t s0, s1;
+      if (values) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          codes[k >> 1][k & 1] =
+              *reinterpret_cast<const uint32_t *>(tile + TL::v_code(at, pr * 32 + 8 * k));
+        s0 = tile[TL::v_scale(at, 2 * pr)];
+        s1 = tile[TL::v_scale(at, 2 * pr + 1)];
+      } else {
+        const uint4 c = *reinterpret_cast<const uint4 *>(tile + TL::k_code(at, pr * 32));
+        codes[0][0] = c.x; codes[0][1] = c.y; codes[1][0] = c.z; codes[1][1] = c.w;
+        s0 = *reinterpret_cast<const uint16_t *>(tile + TL::k_scale(at, 2 * pr));
+        s1 = s0 >> 8;
+      }
+      decode16<T>(codes[0], s0, t, w);
+      decode16<T>(codes[1], s1, t, w + WORDS / 2);
+    } else {  // padding (slot < 0) and slots past the cache read as zeros
+#pragma unroll
+      for (int k = 0; k < WORDS; ++k) w[k] = 0u;
+    }
+#pragma unroll
+    for (int k = 0; k < WORDS / 8; ++k)
+      store32(reinterpret_cast<char *>(row) + 32 * k, a.wide, w + 8 * k);
+  }
+}
+
+template <typename T, int D, bool APPEND>
+cudaError_t rows_t(RowArgs a, int64_t num_tokens, cudaStream_t stream) {
+  // thread numbers are 32-bit: long calls go in parts of at most 2^30 threads
+  const int64_t per8 = int64_t(8) * (D / 32) * a.heads;
+  const int64_t most = std::max<int64_t>(1, (int64_t(1) << 30) / per8) * 8;
+  for (int64_t t0 = 0; t0 < num_tokens; t0 += most) {
+    RowArgs part = a;
+    part.num_tokens = static_cast<int>(std::min(most, num_tokens - t0));
+    const int64_t skip = t0 * a.heads * D * Elt<T>::bytes;
+    part.k_rows = static_cast<const char *>(a.k_rows) + skip;
+    part.v_rows = static_cast<const char *>(a.v_rows) + skip;
+    part.slots = a.slots + t0;
+    const int64_t threads = (part.num_tokens + 7) / 8 * per8;
+    if (threads >= (int64_t(1) << 32)) return cudaErrorInvalidValue;
+    rows_kernel<T, D, APPEND><<<dim3(static_cast<unsigned>((threads + 255) / 256), 2), 256, 0,
+                                stream>>>(part);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+template <typename T, bool APPEND>
+cudaError_t rows_d(int D, const RowArgs &a, int64_t num_tokens, cudaStream_t stream) {
   switch (D) {
-    case 64: return rows_t<T, 64>(append, a, sm_count, stream);
-    case 128: return rows_t<T, 128>(append, a, sm_count, stream);
-    case 256: return rows_t<T, 256>(append, a, sm_count, stream);
+    case 64: return rows_t<T, 64, APPEND>(a, num_tokens, stream);
+    case 128: return rows_t<T, 128, APPEND>(a, num_tokens, stream);
+    case 256: return rows_t<T, 256, APPEND>(a, num_tokens, stream);
     default: return cudaErrorInvalidValue;
   }
 }
 
-cudaError_t rows(bool append, pkv_dtype dtype, int D, const RowArgs &a, int sm_count,
+template <bool APPEND>
+cudaError_t rows(pkv_dtype dtype, int D, const RowArgs &a, int64_t num_tokens,
                  cudaStream_t stream) {
-  if (a.num_tokens == 0) return cudaSuccess;
   switch (dtype) {
-    case PKV_F32: return rows_d<float>(append, D, a, sm_count, stream);
-    case PKV_BF16: return rows_d<__nv_bfloat16>(append, D, a, sm_count, stream);
-    case PKV_F16: return rows_d<__half>(append, D, a, sm_count, stream);
+    case PKV_F32: return rows_d<float, APPEND>(D, a, num_tokens, stream);
+    case PKV_BF16: return rows_d<__nv_bfloat16, APPEND>(D, a, num_tokens, stream);
+    case PKV_F16: return rows_d<__half, APPEND>(D, a, num_tokens, stream);
     default: return cudaErrorInvalidValue;
   }
+}
+
+RowArgs row_args(const void *k_rows, const void *v_rows, const void *k_cache, const void *v_cache,
+                 const int64_t *slots, int num_kv_heads, int64_t num_blocks, float k_scale,
+                 float v_scale, int32_t *err) {
+  const int wide =
+      ((reinterpret_cast<uintptr_t>(k_rows) | reinterpret_cast<uintptr_t>(v_rows)) & 31) == 0;
+  return RowArgs{k_rows, v_rows, static_cast<uint8_t *>(const_cast<void *>(k_cache)),
+                 static_cast<uint8_t *>(const_cast<void *>(v_cache)), slots, num_blocks, 0,
+                 num_kv_heads, k_scale, v_scale, 1.f / k_scale, 1.f / v_scale, wide, err};
 }
 
 }  // namespace
@@ -250,20 +291,21 @@ cudaError_t append_fp4_launch(pkv_dtype src_dtype, const void *k_new, const void
                               void *k_cache, void *v_cache, const int64_t *slots,
                               int64_t num_tokens, int num_kv_heads, int head_dim,
                               int64_t num_blocks, float k_scale, float v_scale, int32_t *err,
-                              int sm_count, cudaStream_t stream) {
-  const fp4::RowArgs a{k_new, v_new, nullptr, nullptr, k_cache, v_cache, slots, num_tokens,
-                       num_blocks, num_kv_heads, k_scale, v_scale, err};
-  return fp4::rows(true, src_dtype, head_dim, a, sm_count, stream);
+                              cudaStream_t stream) {
+  return fp4::rows<true>(src_dtype, head_dim,
+                         fp4::row_args(k_new, v_new, k_cache, v_cache, slots, num_kv_heads,
+                                       num_blocks, k_scale, v_scale, err),
+                         num_tokens, stream);
 }
 
 cudaError_t load_fp4_launch(pkv_dtype out_dtype, void *k_out, void *v_out, const void *k_cache,
                             const void *v_cache, const int64_t *slots, int64_t num_tokens,
                             int num_kv_heads, int head_dim, int64_t num_blocks, float k_scale,
-                            float v_scale, int32_t *err, int sm_count, cudaStream_t stream) {
-  const fp4::RowArgs a{nullptr, nullptr, k_out, v_out, const_cast<void *>(k_cache),
-                       const_cast<void *>(v_cache), slots, num_tokens, num_blocks, num_kv_heads,
-                       k_scale, v_scale, err};
-  return fp4::rows(false, out_dtype, head_dim, a, sm_count, stream);
+                            float v_scale, int32_t *err, cudaStream_t stream) {
+  return fp4::rows<false>(out_dtype, head_dim,
+                          fp4::row_args(k_out, v_out, k_cache, v_cache, slots, num_kv_heads,
+                                        num_blocks, k_scale, v_scale, err),
+                          num_tokens, stream);
 }
 
 }  // namespace pkv

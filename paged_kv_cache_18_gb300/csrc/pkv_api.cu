@@ -1244,11 +1244,9 @@ pkv_status pkv_kv_append_fp4(const void *k_new, const void *v_new, void *k_cache
                                        num_kv_heads, head_dim, block_size, num_blocks, src_dtype,
                                        k_scale, v_scale, error_word);
   if (st != PKV_OK || num_tokens == 0) return st;
-  int device = 0, sms = 0;
-  if (current_sm_count(&device, &sms) != cudaSuccess) return PKV_ERR_CUDA;
   const cudaError_t e = append_fp4_launch(src_dtype, k_new, v_new, k_cache, v_cache, slot_mapping,
                                           num_tokens, num_kv_heads, head_dim, num_blocks, k_scale,
-                                          v_scale, error_word, sms,
+                                          v_scale, error_word,
                                           reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
@@ -1262,11 +1260,9 @@ pkv_status pkv_kv_load_fp4(void *k_out, void *v_out, const void *k_cache, const 
                                        num_kv_heads, head_dim, block_size, num_blocks, out_dtype,
                                        k_scale, v_scale, error_word);
   if (st != PKV_OK || num_tokens == 0) return st;
-  int device = 0, sms = 0;
-  if (current_sm_count(&device, &sms) != cudaSuccess) return PKV_ERR_CUDA;
   const cudaError_t e = load_fp4_launch(out_dtype, k_out, v_out, k_cache, v_cache, slot_mapping,
                                         num_tokens, num_kv_heads, head_dim, num_blocks, k_scale,
-                                        v_scale, error_word, sms,
+                                        v_scale, error_word,
                                         reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }

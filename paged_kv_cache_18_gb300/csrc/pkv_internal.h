@@ -102,11 +102,11 @@ cudaError_t append_fp4_launch(pkv_dtype src_dtype, const void *k_new, const void
                               void *k_cache, void *v_cache, const int64_t *slots,
                               int64_t num_tokens, int num_kv_heads, int head_dim,
                               int64_t num_blocks, float k_scale, float v_scale, int32_t *err,
-                              int sm_count, cudaStream_t stream);
+                              cudaStream_t stream);
 cudaError_t load_fp4_launch(pkv_dtype out_dtype, void *k_out, void *v_out, const void *k_cache,
                             const void *v_cache, const int64_t *slots, int64_t num_tokens,
                             int num_kv_heads, int head_dim, int64_t num_blocks, float k_scale,
-                            float v_scale, int32_t *err, int sm_count, cudaStream_t stream);
+                            float v_scale, int32_t *err, cudaStream_t stream);
 
 // CUDA-core attention over a 4-bit cache (attn_simt_fp4.cu): rows = query rows
 // per CTA, 1, 2 or 4.

@@ -160,6 +160,58 @@ def test_append_of_a_long_prompt_matches_in_every_byte():
     np.testing.assert_array_equal(dv.cpu().numpy(), vc)
 
 
+@pytest.mark.parametrize("t", [1.0, 0.0091, 1e-30, 1e30, 2.0 ** -126, 1e-40, 6e34,
+                               1.9999998807907104])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_append_over_the_whole_range(t, dtype):
+    # magnitudes from subnormal to the largest, blocks of one magnitude and of
+    # many, values on and beside the codes' borders, signed zeros
+    T, H, D = 48, 2, 64
+    rng = np.random.default_rng(11)
+    with np.errstate(all="ignore"):
+        x = rng.standard_normal((T, H, D)) * 2.0 ** rng.integers(-30, 12, (T, H, D // 16)).repeat(
+            16, -1) * min(t, 1e37)
+        x[:8] = 2.0 ** rng.uniform(-149, 127.9, (8, H, D)) * rng.choice([-1, 1], (8, H, D))
+        ties = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0]) * t * 1.125
+        x[8:16] = rng.choice(np.concatenate([ties, -ties, [0.0, -0.0]]), (8, H, D))
+        x[16:20] = np.nextafter(x[8:12].astype(np.float32), np.float32(0))
+        rows = torch.from_numpy(x.astype(np.float32)).to(TORCH_DT[dtype])
+    shape = pkv.fp4_cache_shape(4, H, D)
+    kc, vc = np.zeros(shape, np.uint8), np.zeros(shape, np.uint8)
+    dk, dv = torch.zeros(shape, dtype=torch.uint8, device=DEV), torch.zeros(
+        shape, dtype=torch.uint8, device=DEV)
+    slots = np.arange(T)
+    pkv.kv_append_fp4(rows.to(DEV), (-rows).to(DEV), dk, dv, torch.from_numpy(slots).to(DEV), t, t)
+    with np.errstate(all="ignore"):
+        fp4.append(kc, vc, rows.float().numpy(), -rows.float().numpy(), slots, t, t)
+    np.testing.assert_array_equal(dk.cpu().numpy(), kc)
+    np.testing.assert_array_equal(dv.cpu().numpy(), vc)
+
+
+def test_rows_at_16_byte_alignment():
+    T, H, D = 19, 2, 64
+    k, v = new_rows(T, H, D, "bf16", 12), new_rows(T, H, D, "bf16", 13)
+
+    def shifted(x):  # the same rows 16 bytes into an allocation
+        flat = torch.empty(x.numel() + 8, dtype=x.dtype, device=DEV)
+        out = flat[8:].view(x.shape)
+        out.copy_(x)
+        assert out.data_ptr() % 32 == 16
+        return out
+
+    shape = pkv.fp4_cache_shape(3, H, D)
+    caches = [torch.zeros(shape, dtype=torch.uint8, device=DEV) for _ in range(4)]
+    slots = torch.arange(T, device=DEV)
+    pkv.kv_append_fp4(k.to(DEV), v.to(DEV), caches[0], caches[1], slots, 0.02, 0.02)
+    pkv.kv_append_fp4(shifted(k), shifted(v), caches[2], caches[3], slots, 0.02, 0.02)
+    assert torch.equal(caches[0], caches[2]) and torch.equal(caches[1], caches[3])
+    outs = [shifted(torch.zeros_like(k)), shifted(torch.zeros_like(v))]
+    pkv.kv_load_fp4(caches[0], caches[1], slots, 0.02, 0.02, k_out=outs[0], v_out=outs[1])
+    want = pkv.kv_load_fp4(caches[0], caches[1], slots, 0.02, 0.02)
+    for got, w in zip(outs, want):
+        assert torch.equal(torch.nan_to_num(got, 9.0), torch.nan_to_num(w, 9.0))
+
+
 def test_slots_past_the_cache_are_recorded_and_left_out():
     H, D, NB = 2, 64, 2
     k = new_rows(3, H, D, "f32").to(DEV)
