@@ -38,11 +38,9 @@ constexpr int kStreamKWeight = 24;
 // The same for the 4-bit cache's tensor-core kernel, its workers being CTAs or
 // warps, the fewest blocks worth a CTA, and the longest batch whose lengths
 // every worker adds up.
-constexpr int kFp4Weight = 32, kFp4WarpWeight = 8;
+constexpr int kFp4Weight = 16, kFp4WarpWeight = 8;
 constexpr int kFp4MinBlocks = 16;
 constexpr int kFp4MaxBatch = 1024;
-// Units from which its workers are warps.
-constexpr int64_t kFp4WarpUnits = 608;
 constexpr size_t kUsableSmemPerSm = 228 * 1024;
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -171,13 +169,12 @@ bool fp4_balanced(const Shape &s, const pkv_options *opt, int64_t units) {
          units * (max_blocks + kFp4Weight) < (int64_t(1) << 31);
 }
 
-// With many units (sequence, KV head, row chunk) each warp is a worker of the
-// balanced partition: a unit is then cut into few pieces all the same, and a
-// piece costs a warp its start and end once instead of four warps.
+// With up to 16 query rows (8 at head_dim 256) each warp is a worker of the
+// balanced partition: a piece costs a warp its start and end once instead of four
+// warps.
 bool fp4_warp_workers(const Shape &s, const pkv_options *opt, int row_chunks, int rows) {
   const int64_t units = static_cast<int64_t>(s.batch) * s.num_kv_heads * row_chunks;
-  return fp4_balanced(s, opt, units) && units >= kFp4WarpUnits &&
-         rows <= 8 * mma_fp4_max_warp_tiles(s.head_dim);
+  return fp4_balanced(s, opt, units) && rows <= 8 * warp_fp4_max_tiles(s.head_dim);
 }
 
 // The same for a 4-bit cache.
@@ -191,16 +188,19 @@ bool choose_fp4_kernel(const Shape &s, const pkv_options *opt, int rows, pkv_pla
   if (kernel == PKV_KERNEL_AUTO) kernel = f32 ? PKV_KERNEL_SIMT : PKV_KERNEL_MMA;
   if (kernel != PKV_KERNEL_SIMT && (kernel != PKV_KERNEL_MMA || f32)) return false;
   const bool mma = kernel == PKV_KERNEL_MMA;
-  int cap = mma ? 8 * mma_fp4_max_tiles(s.head_dim) : simt_fp4_max_rows();
+  int cap = mma ? 8 * cta_fp4_max_tiles(s.head_dim) : simt_fp4_max_rows();
   if (opt && opt->rows_per_cta > 0 && opt->rows_per_cta < cap) cap = opt->rows_per_cta;
   const int chunks = ceil_div(rows, cap);
   const int per_cta = ceil_div(rows, chunks);
   int r = 1;
   while (r < per_cta) r <<= 1;
-  if (mma ? !mma_fp4_kernel_info(s.qdtype, s.head_dim, ceil_div(per_cta, 8),
-                                 fp4_warp_workers(s, opt, chunks, per_cta), info)
-          : !simt_fp4_kernel_info(s.qdtype, s.head_dim, r, info))
-    return false;
+  const int tiles = ceil_div(per_cta, 8);
+  const bool ok =
+      !mma ? simt_fp4_kernel_info(s.qdtype, s.head_dim, r, info)
+      : fp4_warp_workers(s, opt, chunks, per_cta)
+          ? warp_fp4_kernel_info(s.qdtype, s.head_dim, tiles, info)
+          : cta_fp4_kernel_info(s.qdtype, s.head_dim, tiles, info);
+  if (!ok) return false;
   pl->kernel = kernel;
   pl->rows_per_cta = per_cta;
   pl->row_chunks = chunks;
@@ -289,8 +289,12 @@ WorkspaceLayout workspace_layout(const Shape &s, int num_splits, int row_chunks,
                          (stream_k ? static_cast<size_t>(s.batch) * s.num_kv_heads * row_chunks : 0);
     const size_t parts = slots * rows_per_cta;
     w.lse_off = up(parts * s.head_dim * sizeof(float));
-    w.ctr_off = w.lse_off + up(parts * sizeof(float));  // here: the layout per sequence
-    w.total = w.ctr_off + up((static_cast<size_t>(s.batch) * 2 + 2) * sizeof(int));
+    w.ctr_off = w.lse_off + up(parts * sizeof(float));  // here: the layout per sequence,
+    const size_t layout =                               // of a 4-bit cache per unit
+        s.dtype == PKV_FP4_E2M1 && stream_k
+            ? static_cast<size_t>(s.batch) * s.num_kv_heads * row_chunks
+            : static_cast<size_t>(s.batch) + 1;
+    w.total = w.ctr_off + up(layout * 2 * sizeof(int));
     w.fused_merge = false;
     return w;
   }
@@ -642,6 +646,8 @@ pkv_status run_attention(void *out, const void *q, const void *k_cache, const vo
                 : pl.split_target > pl.grid_x ? kFp4WarpWeight : kFp4Weight;
   p.scale_log2 =
       static_cast<float>(static_cast<double>(scale) * 1.4426950408889634 * k_scale);
+  if (s.dtype == PKV_FP4_E2M1)  // positive and finite whatever the scales' product is
+    p.scale_log2 = std::min(std::max(p.scale_log2, 1.17549435e-38f), 3.4028234e38f);
   p.out_scale = v_scale;
   bool merge_kernel = false;
   if (pl.num_splits > 1 || pl.split_target > 0) {
@@ -672,7 +678,10 @@ pkv_status run_attention(void *out, const void *q, const void *k_cache, const vo
     if (e != cudaSuccess) return PKV_ERR_CUDA;
   }
   if (pl.kernel == PKV_KERNEL_MMA && s.dtype == PKV_FP4_E2M1) {
-    e = mma_fp4_launch(s.qdtype, s.head_dim, ceil_div(pl.rows_per_cta, 8), p, grid, stream);
+    const int tiles = ceil_div(pl.rows_per_cta, 8);
+    e = pl.stream_k && pl.split_target > pl.grid_x
+            ? warp_fp4_launch(s.qdtype, s.head_dim, tiles, p, grid, stream)
+            : cta_fp4_launch(s.qdtype, s.head_dim, tiles, p, grid, stream);
   } else if (pl.kernel == PKV_KERNEL_MMA) {
     CUtensorMap kmap, vmap;
     p.tile_box =
@@ -701,7 +710,9 @@ pkv_status run_attention(void *out, const void *q, const void *k_cache, const vo
   }
   if (e != cudaSuccess) return PKV_ERR_CUDA;
   if (merge_kernel) {
-    e = merge_launch(s.qdtype, s.head_dim, p, sms, stream);
+    e = s.dtype == PKV_FP4_E2M1 && pl.stream_k
+            ? merge_fp4_launch(s.qdtype, s.head_dim, p, sms, stream)
+            : merge_launch(s.qdtype, s.head_dim, p, sms, stream);
     if (e != cudaSuccess) return PKV_ERR_CUDA;
   }
   return PKV_OK;

@@ -115,16 +115,21 @@ bool simt_fp4_kernel_info(pkv_dtype q_dtype, int head_dim, int rows, KernelInfo 
 cudaError_t simt_fp4_launch(pkv_dtype q_dtype, int head_dim, int rows, const AttnParams &p,
                             dim3 grid, cudaStream_t stream);
 
-// Tensor-core attention over a 4-bit cache (attn_fp4.cu): bf16 / f16 q, `tiles`
-// 8-column tiles of query rows per worker.  Workers of the balanced partition
-// are CTAs, or (warp_workers, up to mma_fp4_max_warp_tiles; p.split_target is
-// then 4 times the grid) warps.
-int mma_fp4_max_tiles(int head_dim);
-int mma_fp4_max_warp_tiles(int head_dim);
-bool mma_fp4_kernel_info(pkv_dtype q_dtype, int head_dim, int tiles, bool warp_workers,
-                         KernelInfo *info);
-cudaError_t mma_fp4_launch(pkv_dtype q_dtype, int head_dim, int tiles, const AttnParams &p,
+// Tensor-core attention over a 4-bit cache: bf16 / f16 q, `tiles` 8-column tiles
+// of query rows per worker.  Workers are CTAs (attn_fp4_cta.cu: every split
+// plan) or warps (attn_fp4_warp.cu: the balanced partition with p.split_target =
+// 4 times the grid).
+int cta_fp4_max_tiles(int head_dim);
+bool cta_fp4_kernel_info(pkv_dtype q_dtype, int head_dim, int tiles, KernelInfo *info);
+cudaError_t cta_fp4_launch(pkv_dtype q_dtype, int head_dim, int tiles, const AttnParams &p,
                            dim3 grid, cudaStream_t stream);
+// The merge of the balanced partition's partials (merge_fp4.cu).
+cudaError_t merge_fp4_launch(pkv_dtype dtype, int head_dim, const AttnParams &p, int sm_count,
+                             cudaStream_t stream);
+int warp_fp4_max_tiles(int head_dim);
+bool warp_fp4_kernel_info(pkv_dtype q_dtype, int head_dim, int tiles, KernelInfo *info);
+cudaError_t warp_fp4_launch(pkv_dtype q_dtype, int head_dim, int tiles, const AttnParams &p,
+                            dim3 grid, cudaStream_t stream);
 
 // Row moves after a verified tree (commit_rows.cu): every cache tensor of a
 // list in one launch; the first `first_value` of it hold keys (the 4-bit tiles

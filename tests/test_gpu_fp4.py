@@ -270,16 +270,18 @@ def test_row_chunks(kernel, rows):
                    seed=2150), kernel=kernel, rows_per_cta=rows)
 
 
-@pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("Q,Hq,Hkv,tiles,chunks", [(2, 8, 2, 1, 1), (3, 8, 2, 2, 1),
-                                                   (5, 8, 2, 3, 1), (8, 8, 2, 4, 1),
-                                                   (10, 8, 2, 5, 1), (11, 8, 2, 3, 2),
-                                                   (31, 4, 1, 4, 4)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Q,Hq,Hkv", [(2, 8, 2), (3, 8, 2), (5, 8, 2), (8, 8, 2), (10, 8, 2),
+                                      (11, 8, 2), (13, 8, 2), (31, 4, 1), (64, 3, 1)])
 @pytest.mark.parametrize("split_blocks", [0, 5])
-def test_every_column_tile(D, Q, Hq, Hkv, tiles, chunks, split_blocks):
+def test_every_column_tile(D, Q, Hq, Hkv, split_blocks):
     lens = [Q, Q + 1, Q + 40, 333, 1200]
+    cap, built = (64, (1, 2, 3, 4, 5, 6, 8)) if D <= 128 else (32, (1, 2, 4))
+    rows = Q * Hq // Hkv
+    chunks = -(-rows // cap)
+    tiles = -(-(-(-rows // chunks)) // 8)
     p = pkv.plan(len(lens), Q, Hq, Hkv, D, max(lens), "fp4", split_blocks=split_blocks)
-    assert (p["warp_tiles"], p["row_chunks"]) == (tiles, chunks)
+    assert p["row_chunks"] == chunks and p["warp_tiles"] == min(n for n in built if n >= tiles)
     run(W.Workload("fp4 tiles", len(lens), Hq, Hkv, D, "bf16", context_lens=lens, num_queries=Q,
                    seed=2155 + Q), split_blocks=split_blocks)
 
@@ -330,6 +332,14 @@ def test_tensor_scales(k_scale, v_scale):
     # saturating, underflowing and far-off scales: the codes are what counts
     run(W.Workload("fp4 scales", 3, 8, 2, 128, "f32", context_lens=[10, 90, 300], seed=2200),
         k_scale=k_scale, v_scale=v_scale)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_vanishing_scores_average_the_values(dtype):
+    # softmax scale times key scale below the smallest float: all weights equal
+    wl = W.Workload("fp4 vanishing", 2, 8, 2, 64, dtype, context_lens=[20, 700], seed=2205,
+                    scale=1e-30)
+    run(wl, k_scale=1e-20, v_scale=0.01)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
