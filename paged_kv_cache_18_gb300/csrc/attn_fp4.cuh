@@ -11,9 +11,12 @@
 namespace pkv {
 namespace fp4 {
 constexpr int kWarps = 4;  // warps of a CTA
-// Weights against a column's reference stay below 2^kSlack, well inside f16; the
-// larger, the rarer a new reference.
-constexpr float kSlack = 14.f, kHeaviest = 16384.f;
+// Weights enter the MMAs in f16, against a reference per column that is raised
+// when one exceeds 2^kSlack, to where the largest weight seen is 2^kHead: above 1,
+// so that the weights of a long flat tail keep their bits (f16 holds 2^-14 of the
+// largest at 11 bits, and drops what is below 2^-24 - kHead of it), and far enough
+// below the slack that raising stays rare.
+constexpr float kSlack = 14.f, kHeaviest = 16384.f, kHead = 6.f;
 constexpr float kNothing = -3e38f;  // reference of a column that has seen no row: finite,
                                     // so that -inf scores still weigh 0 against it
 
@@ -75,7 +78,8 @@ __device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4],
 }
 
 // Scores of UB blocks that lie one after another (key tile, value tile) from
-// shared address `blk`: S^T[16 keys x 8 NT] = K Q^T of each; `q(ks, nt, b0, b1)` gives the Q^T fragment of a k-step and tile.
+// shared address `blk`: S^T[16 keys x 8 NT] = K Q^T of each; `q(ks, nt, b0, b1)`
+// gives the Q^T fragment of a k-step and tile.
 // Lane (g, c) reads 32 dims of each panel of its two keys; k-step (panel, word w,
 // half e) holds dims  panel + 8 WP c + 8 w + 4 e + {0, 1 | 2, 3}.
 template <int D> struct Lanes {
@@ -211,14 +215,12 @@ __device__ __forceinline__ void map_columns(const AttnParams &p, int chunk, int 
   __syncwarp();
 }
 
+constexpr int kMinPlaces = 16;  // of a worker
+
 // The pieces of work of a worker (a CTA or a warp), in turn: one under the
 // host's and the device's split partitions (cta_work), under the balanced one
 // the parts of units in its range of the list (sk_begin, pkv_device.cuh).
 // Warp-collective; the warps of a CTA that is a worker walk alike.
-constexpr int kMinPlaces = 16;  // of a worker
-
-// The walk's state and the pieces lie in shared memory, one copy a warp: they
-// are needed between pieces only, where registers are scarce.
 struct Piece {
   int b, kvh, chunk, L;
   int blk_begin, blk_end;

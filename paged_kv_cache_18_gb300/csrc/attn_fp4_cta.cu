@@ -389,9 +389,10 @@ __global__ void __launch_bounds__(kWarps * 32, (CtaShape<D, NT>::kMinCtas))
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int col = nt * 8 + 2 * c + e;
-            float m_new = m[nt][e];
+            float top = s_top[0][col];
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) m_new = fmaxf(m_new, s_top[w][col]);
+            for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_top[w][col]);
+            const float m_new = fmaxf(m[nt][e], top - kHead / fac[nt][e]);
             const float corr = ex2((m[nt][e] - m_new) * fac[nt][e]);
             l[nt][e] *= corr;
             m[nt][e] = m_new;

@@ -208,7 +208,17 @@ __global__ void __launch_bounds__(kWarps * 32) simt_kernel(const AttnParams p) {
     }
   }
   __syncthreads();
-  cta_epilogue<TQ, D, R, kWarps, kWarps * 32, true>(p, red_m, red_l, red_o, wscale, wk);
+  cta_epilogue<TQ, D, R, kWarps, kWarps * 32>(p, red_m, red_l, red_o, wscale, wk);
+  // A partial whose sum is NaN (a NaN scale in the cache) has to reach the merged
+  // row: its log-sum-exp is +inf, not that of a row that sees nothing.
+  if (p.num_splits == 1 && p.split_target == 0) return;
+  __syncthreads();
+  const int64_t row = threadIdx.x < R ? cta_row_index(p, b, kvh, chunk, threadIdx.x) : -1;
+  if (row < 0) return;
+  float sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) sum += red_l[w * R + threadIdx.x];
+  if (isnan(sum)) p.part_lse[partial_index(p, wk, row, threadIdx.x)] = INFINITY;
 }
 
 template <int D, int R> constexpr size_t simt_smem() {

@@ -592,9 +592,7 @@ __device__ __forceinline__ bool split_arrive(const AttnParams &p, int b, int kvh
 //   - otherwise this split's normalised output and its log-sum-exp, and, with
 //     counters, the CTA that completes the sequence's splits merges them
 //     (the Flash-Decoding reduction: weights 2^(lse_s - max lse)).
-// NANS: a row whose sum is NaN leaves a partial of log-sum-exp +inf, which makes
-// the merged row NaN (else it counts as a row that sees nothing).
-template <typename T, int D, int NC, int W, int NTHR, bool NANS = false>
+template <typename T, int D, int NC, int W, int NTHR>
 __device__ __forceinline__ void cta_epilogue(const AttnParams &p, float *red_m, float *red_l,
                                              float *red_o, float *wscale, const CtaWork &wk) {
   const int b = wk.b, kvh = wk.kvh, chunk = wk.chunk, ns_b = wk.ns_b;
@@ -615,8 +613,7 @@ __device__ __forceinline__ void cta_epilogue(const AttnParams &p, float *red_m, 
       lsum += red_l[w * NC + tid] * s;
     }
     wscale[W * NC + tid] = lsum > 0.f ? 1.f / lsum : 0.f;
-    wscale[(W + 1) * NC + tid] =
-        lsum > 0.f ? M + __log2f(lsum) : (NANS && lsum != 0.f ? INFINITY : -INFINITY);
+    wscale[(W + 1) * NC + tid] = lsum > 0.f ? M + __log2f(lsum) : -INFINITY;
   }
   __syncthreads();
   // (the device partition always leaves partials for the merge kernel)

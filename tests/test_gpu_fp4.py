@@ -335,6 +335,44 @@ def test_tensor_scales(k_scale, v_scale):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("Q,split_blocks", [(1, 0), (1, 100000), (5, 0)])
+def test_a_peak_over_a_long_flat_tail(dtype, Q, split_blocks):
+    # one key scores 20 bits above 40000 equal ones, which together weigh 5 % of
+    # it: every weight of the tail has to keep its bits (rounded to a multiple of
+    # 2^-24 of the peak each would be off by 3 %, the result by 1e-3)
+    D, L = 64, 40000
+    NB = -(-L // 16)
+    k = np.zeros((NB, 1, 16, D), np.float32)
+    v = np.ones((NB, 1, 16, D), np.float32)
+    k[7, 0, 3, 0] = 6.0
+    v[7, 0, 3] = -0.5
+    kc, vc = fp4.pack(k, 1.0, True), fp4.pack(v, 1.0, False)
+    q = np.zeros((1, Q, 2, D), np.float32)
+    scale = 0.125
+    q[..., 0] = 19.55 * math.log(2.0) / 6.0 / scale
+    qt = torch.from_numpy(q).to(TORCH_DT[dtype])
+    table, lens = np.arange(NB, dtype=np.int32)[None], np.array([L], np.int32)
+    got = pkv.paged_attention_fp4((qt if Q > 1 else qt[:, 0]).contiguous().to(DEV),
+                                  torch.from_numpy(kc).to(DEV), torch.from_numpy(vc).to(DEV),
+                                  torch.from_numpy(table).to(DEV), torch.from_numpy(lens).to(DEV),
+                                  1.0, 1.0, scale=scale, max_context_len=L,
+                                  split_blocks=split_blocks)
+    ref = fp4.attention(qt.float().numpy(), kc, vc, table, lens, scale, 1.0, 1.0)
+    got = got.double().cpu().numpy().reshape(ref.shape)
+    # the output's rounding, the exponentials' argument (20 bits at 2^-24 relative),
+    # the float32 sums, and the weights' 2^-11 (the peak's own)
+    tol = half_ulp(ref, dtype) + 20 * 2.0 ** -23
+    if dtype == "f32":
+        # A warp adds every fourth block key by key.  Its running numerator is at most
+        # 0.5 + 0.013, so each of its L / 4 additions is off by at most 2^-25; its sum of
+        # weights is below 2, and gets one addition a block, off by at most 2^-24.
+        tol = tol + L / 4 * 2.0 ** -25 + L / 64 * 2.0 ** -24
+    else:
+        tol = tol + L * 2.0 ** -24 * 0.04 + 2.0 ** -11 * 0.04 + 2.0 ** -14 * 0.5
+    assert (np.abs(got - ref) <= tol).all(), np.abs(got - ref).max()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 def test_vanishing_scores_average_the_values(dtype):
     # softmax scale times key scale below the smallest float: all weights equal
     wl = W.Workload("fp4 vanishing", 2, 8, 2, 64, dtype, context_lens=[20, 700], seed=2205,
