@@ -78,20 +78,23 @@ __device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4],
 }
 
 // Scores of UB blocks that lie one after another (key tile, value tile) from
-// shared address `blk`: S^T[16 keys x 8 NT] = K Q^T of each; `q(ks, nt, b0, b1)`
-// gives the Q^T fragment of a k-step and tile.
+// shared address `blk`: S^T[16 keys x 8 NT] = K Q^T of each; `q(ks, nt, part, b0, b1)`
+// gives the Q^T fragment of a k-step and tile.  Queries in PARTS f16 parts
+// (split_row): the products with the small parts have a sum of their own, so that
+// the large one sees as few roundings as with one part.
 // Lane (g, c) reads 32 dims of each panel of its two keys; k-step (panel, word w,
 // half e) holds dims  panel + 8 WP c + 8 w + 4 e + {0, 1 | 2, 3}.
 template <int D> struct Lanes {
   static constexpr int WP = Tile<D>::kPanel / 32;  // words (8 dims) of a lane in a panel
   static constexpr int KSP = 2 * WP;               // k-steps of a panel
 };
-template <int D, int NT, int UB, typename Q>
+template <int D, int NT, int UB, int PARTS = 1, typename Q>
 __device__ __forceinline__ void block_scores(float (&sc)[UB][NT][4], uint32_t blk, int g, int c,
                                              const Q &q) {
   using TL = Tile<D>;
   constexpr int WP = Lanes<D>::WP, KSP = Lanes<D>::KSP;
   const int kk = key_of(g);
+  float low[PARTS > 1 ? UB : 1][PARTS > 1 ? NT : 1][4];
 #pragma unroll
   for (int pn = 0; pn < TL::kPanels; ++pn) {
     uint32_t w0[UB][WP], w1[UB][WP], s0[UB][2], s1[UB][2];
@@ -139,16 +142,34 @@ __device__ __forceinline__ void block_scores(float (&sc)[UB][NT][4], uint32_t bl
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           uint32_t b0, b1;
-          q(ks, nt, b0, b1);
+          q(ks, nt, 0, b0, b1);
 #pragma unroll
           for (int u = 0; u < UB; ++u) {
             if (ks == 0) mma_first(sc[u][nt], a[u], b0, b1);
             else Mma<__half>::run(sc[u][nt], a[u], b0, b1);
           }
+          if constexpr (PARTS > 1) {
+#pragma unroll
+            for (int part = PARTS - 1; part > 0; --part) {
+              q(ks, nt, part, b0, b1);
+#pragma unroll
+              for (int u = 0; u < UB; ++u) {
+                if (ks == 0 && part == PARTS - 1) mma_first(low[u][nt], a[u], b0, b1);
+                else Mma<__half>::run(low[u][nt], a[u], b0, b1);
+              }
+            }
+          }
         }
       }
     }
   }
+  if constexpr (PARTS > 1)
+#pragma unroll
+    for (int u = 0; u < UB; ++u)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[u][nt][e] += low[u][nt][e];
 }
 
 // Make the value scales of rows nv .. 15 of a block zero (tile: its key tile,
@@ -194,6 +215,43 @@ __device__ __forceinline__ float convert_row(uint32_t (&f)[WORDS], float scale_l
     // (kept positive and finite: 0 and infinity would make NaN of masked scores)
     return fminf(fmaxf(scale_log2 * __int_as_float((127 - qshift) << 23), kTiny), kHuge);
   }
+}
+
+// Two float32 values as three f16 pairs: x = hi + mid + lo, to 2^-25 absolute.  An
+// infinity or NaN is the first part's alone.
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t (&part)[3]) {
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    part[k] = Mma<__half>::pack(x, y);
+    float hx, hy;
+    Mma<__half>::unpack(part[k], hx, hy);
+    x = isfinite(x) ? x - hx : 0.f;  // (exact)
+    y = isfinite(y) ? y - hy : 0.f;
+  }
+}
+
+// A float32 query row as f16 operands in three parts: shifted by a power of two so
+// that its largest magnitude lies in [2^14, 2^15), an element keeps its 24 bits
+// down to 2^-14 of the largest and is off by 2^-39 of that below.  Returns the row's
+// score factor (convert_row).  Warp-collective.
+template <int PER>
+__device__ __forceinline__ float split_row(const uint32_t (&f)[PER],
+                                           uint32_t (&parts)[3][PER / 2], float scale_log2) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) top = max(top, f[k] & 0x7fffffffu);
+  top = __reduce_max_sync(kFull, top);
+  const int ex = top > 0 ? static_cast<int>(top >> 23) - 126 : 15;
+  const int qshift = max(-120, min(120, 15 - ex));
+  const float up = __int_as_float((127 + qshift) << 23);
+#pragma unroll
+  for (int k = 0; k < PER; k += 2) {
+    uint32_t part[3];
+    split_pair(__uint_as_float(f[k]) * up, __uint_as_float(f[k + 1]) * up, part);
+#pragma unroll
+    for (int j = 0; j < 3; ++j) parts[j][k / 2] = part[j];
+  }
+  return fminf(fmaxf(scale_log2 * __int_as_float((127 - qshift) << 23), kTiny), kHuge);
 }
 
 // The query rows of a piece: how many, the first one's flat index (of j = 0, its

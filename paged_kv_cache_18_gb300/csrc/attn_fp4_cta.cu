@@ -33,26 +33,29 @@ namespace pkv {
 namespace fp4 {
 namespace {
 
-template <int D, int NT> struct CtaShape {
-  static constexpr int UW = NT <= 4 ? 2 : 1;  // blocks of a group that are a warp's
-  static constexpr int kGroup = UW * kWarps;  // blocks of a group
-  static constexpr int NS = NT <= 4 ? 2 : 4;  // groups in the ring
-  static constexpr bool kRegQ = NT <= 2 && D <= 128;  // Q^T fragments in registers
+template <typename T, int D, int NT> struct CtaShape {
+  static constexpr bool kF32 = std::is_same<T, float>::value;
+  static constexpr int kParts = kF32 ? 3 : 1;  // f16 parts of a query element and a weight
+  static constexpr int UW = NT <= (kF32 ? 2 : 4) ? 2 : 1;  // blocks of a group that are a warp's
+  static constexpr int kGroup = UW * kWarps;               // blocks of a group
+  static constexpr int NS = UW == 2 ? 2 : 4;               // groups in the ring
+  static constexpr bool kRegQ = NT <= 2 && D <= 128 && !kF32;  // Q^T fragments in registers
   // blocks whose scores are computed together, each Q^T fragment loaded once
-  static constexpr int UB = !kRegQ && NT <= 4 && D <= 128 ? UW : 1;
+  static constexpr int UB = !kRegQ && NT <= 4 && D <= 128 && !kF32 ? UW : 1;
   static constexpr bool kRegFac = NT <= 4;    // score factors in registers
   // resident CTAs it is compiled for
-  static constexpr int kMinCtas = D == 256 ? 1 : (NT >= 6 ? 2 : 3);
+  static constexpr int kMinCtas = D == 256 ? 1 : (NT >= (kF32 ? 3 : 6) ? 2 : 3);
 };
 
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, (CtaShape<D, NT>::kMinCtas))
+__global__ void __launch_bounds__(kWarps * 32, (CtaShape<T, D, NT>::kMinCtas))
     cta_kernel(const AttnParams p) {
   pdl_wait();
   using TL = Tile<D>;
   using MM = Mma<__half>;
-  using SH = CtaShape<D, NT>;
-  constexpr int NS = SH::NS, UW = SH::UW, kGroup = SH::kGroup;
+  using SH = CtaShape<T, D, NT>;
+  constexpr int NS = SH::NS, UW = SH::UW, kGroup = SH::kGroup, PARTS = SH::kParts;
+  constexpr bool F32 = SH::kF32;
   constexpr bool QR = SH::kRegQ;
   constexpr int NC = NT * 8;
   constexpr int PAIR = 2 * TL::kBytes;  // a block's key and value tiles
@@ -65,8 +68,9 @@ __global__ void __launch_bounds__(kWarps * 32, (CtaShape<D, NT>::kMinCtas))
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
   const uint32_t ring = smem_u32(smem);
-  const uint32_t q_smem = ring + NS * STAGE;           // [ks][nt][lane] fragments of Q^T
-  uint8_t *const p_frags = smem + NS * STAGE + KS * NT * 256;  // [2][block][nt][lane] of P^T
+  const uint32_t q_smem = ring + NS * STAGE;           // [part][ks][nt][lane] fragments of Q^T
+  constexpr int P_BLOCK = PARTS * NT * 256;
+  uint8_t *const p_frags = smem + NS * STAGE + PARTS * KS * NT * 256;  // [2][block][part][nt][lane] of P^T
   __shared__ uint64_t bars[NS];
   __shared__ __align__(8) float s_fac[NC];             // score factor per column
   __shared__ int s_row[kWarps][NC], s_j[kWarps][NC];   // map_columns
@@ -87,14 +91,14 @@ __global__ void __launch_bounds__(kWarps * 32, (CtaShape<D, NT>::kMinCtas))
   Piece wk;
   if (!walk.first(p, blockIdx.x, &wk)) return;  // (the whole CTA agrees)
   if (threadIdx.x == 0) s_piece[0] = wk;
-  for (int k = threadIdx.x; k < KS * NT * 32; k += kWarps * 32)  // columns without a row: 0
+  for (int k = threadIdx.x; k < PARTS * KS * NT * 32; k += kWarps * 32)  // columns without a row: 0
     if (k / 32 % NT * 8 + (k & 31) / 4 >= p.rows_per_cta)
       asm volatile("st.shared.v2.u32 [%0], {%1,%1};" ::"r"(q_smem + k * 8), "r"(0) : "memory");
 
   // A piece's query rows, every fourth by this warp, D / 32 dims a lane.  For
   // the first piece they are loaded before the ring's copies, behind which they
   // would queue (5 us at the start of a call).
-  constexpr int PER = D / 32, WORDS = PER / 2, Q_ROWS = NC / kWarps;
+  constexpr int PER = D / 32, WORDS = F32 ? PER : PER / 2, Q_ROWS = NC / kWarps;
   uint32_t q_raw[Q_ROWS][WORDS];
   auto load_rows = [&](const Piece &w) {
     const int n = rows_of(p, w.chunk);
@@ -189,7 +193,15 @@ __global__ void __launch_bounds__(kWarps * 32, (CtaShape<D, NT>::kMinCtas))
     for (int k = 0; k < Q_ROWS; ++k) {
       const int col = k * kWarps + warp;
       if (col >= n_rows) break;
-      const float fac = convert_row<T>(q_raw[k], p.scale_log2);
+      uint32_t parts[PARTS][PER / 2];
+      float fac;
+      if constexpr (F32) {
+        fac = split_row<PER>(q_raw[k], parts, p.scale_log2);
+      } else {
+        fac = convert_row<T>(q_raw[k], p.scale_log2);
+#pragma unroll
+        for (int e = 0; e < WORDS; ++e) parts[0][e] = q_raw[k][e];
+      }
       constexpr int HALVES = PER > 4 ? PER / 4 : 1;  // fragments of four dims (or a half)
 #pragma unroll
       for (int e = 0; e < HALVES; ++e) {
@@ -197,11 +209,14 @@ __global__ void __launch_bounds__(kWarps * 32, (CtaShape<D, NT>::kMinCtas))
         const int ks = d / TL::kPanel * KSP + in % (8 * WP) / 4, cq = in / (8 * WP);
         const uint32_t at =
             q_smem + (ks * NT + (col >> 3)) * 256 + ((col & 7) * 4 + cq) * 8 + d % 4 * 2;
+        constexpr int PAIRS = PER / 2 / HALVES;
 #pragma unroll
-        for (int x = 0; x < WORDS / HALVES; ++x)
-          asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 4 * x),
-                       "r"(q_raw[k][e * (WORDS / HALVES) + x])
-                       : "memory");
+        for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+          for (int x = 0; x < PAIRS; ++x)
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + part * (KS * NT * 256) + 4 * x),
+                         "r"(parts[part][e * PAIRS + x])
+                         : "memory");
       }
       if (lane == 0) s_fac[col] = fac;
     }
@@ -227,12 +242,12 @@ __global__ void __launch_bounds__(kWarps * 32, (CtaShape<D, NT>::kMinCtas))
           qf[ks][nt][1] = x.y;
         }
     }
-    auto q_frag = [&](int ks, int nt, uint32_t &b0, uint32_t &b1) {
+    auto q_frag = [&](int ks, int nt, int part, uint32_t &b0, uint32_t &b1) {
       if constexpr (QR) {
         b0 = qf[ks][nt][0];
         b1 = qf[ks][nt][1];
       } else {
-        const uint2 x = lds64(q_smem + (ks * NT + nt) * 256 + lane * 8);
+        const uint2 x = lds64(q_smem + ((part * KS + ks) * NT + nt) * 256 + lane * 8);
         b0 = x.x;
         b1 = x.y;
       }
@@ -310,7 +325,7 @@ __global__ void __launch_bounds__(kWarps * 32, (CtaShape<D, NT>::kMinCtas))
       float sc[UW][NT][4];
 #pragma unroll
       for (int u = 0; u < UW; u += UB)
-        block_scores<D, NT, UB>(reinterpret_cast<float(&)[UB][NT][4]>(sc[u]), tile + u * PAIR, g, c,
+        block_scores<D, NT, UB, PARTS>(reinterpret_cast<float(&)[UB][NT][4]>(sc[u]), tile + u * PAIR, g, c,
                                 q_frag);
       if (edge) {
         const int kk = key_of(g);
@@ -338,7 +353,7 @@ __global__ void __launch_bounds__(kWarps * 32, (CtaShape<D, NT>::kMinCtas))
       // never raises it, and reaches O through its weight.)
       float sum[NT][2];
       uint8_t *const p_at =
-          p_frags + (turn & 1) * (kGroup * NT * 256) + warp * UW * (NT * 256) + lane * 8;
+          p_frags + (turn & 1) * (kGroup * P_BLOCK) + warp * UW * P_BLOCK + lane * 8;
       float heaviest = 0.f;
       auto weights = [&]() {
 #pragma unroll
@@ -353,8 +368,18 @@ __global__ void __launch_bounds__(kWarps * 32, (CtaShape<D, NT>::kMinCtas))
             sum[nt][0] += w[0] + w[2];
             sum[nt][1] += w[1] + w[3];
             heaviest = fmaxf(heaviest, fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3])));
-            *reinterpret_cast<uint2 *>(p_at + (u * NT + nt) * 256) =
-                make_uint2(movm_t(MM::pack(w[0], w[1])), movm_t(MM::pack(w[2], w[3])));
+            if constexpr (F32) {
+              uint32_t a[3], b[3];
+              split_pair(w[0], w[1], a);
+              split_pair(w[2], w[3], b);
+#pragma unroll
+              for (int k = 0; k < 3; ++k)
+                *reinterpret_cast<uint2 *>(p_at + u * P_BLOCK + (k * NT + nt) * 256) =
+                    make_uint2(movm_t(a[k]), movm_t(b[k]));
+            } else {
+              *reinterpret_cast<uint2 *>(p_at + u * P_BLOCK + nt * 256) =
+                  make_uint2(movm_t(MM::pack(w[0], w[1])), movm_t(MM::pack(w[2], w[3])));
+            }
           }
         }
       };
@@ -414,7 +439,10 @@ __global__ void __launch_bounds__(kWarps * 32, (CtaShape<D, NT>::kMinCtas))
       // its stage takes the next copies.  (NS groups in flight and this one.)
       if (turn_in - turn < NS) copy_group(which);
       // O^T += V^T P^T over the group, for this warp's dims.
-      const uint8_t *const p_in = p_frags + (turn & 1) * (kGroup * NT * 256) + lane * 8;
+      const uint8_t *const p_in = p_frags + (turn & 1) * (kGroup * P_BLOCK) + lane * 8;
+      // (float32: the group's products have a sum of their own, so that a long
+      // context is not a long chain of the MMA's roundings)
+      float part_sum[F32 ? MT : 1][F32 ? NT : 1][4];
 #pragma unroll
       for (int u = 0; u < kGroup; ++u) {
         constexpr uint32_t LOW = 0x0f0f0f0fu;
@@ -453,10 +481,29 @@ __global__ void __launch_bounds__(kWarps * 32, (CtaShape<D, NT>::kMinCtas))
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const uint2 b = *reinterpret_cast<const uint2 *>(p_in + (u * NT + nt) * 256);
 #pragma unroll
-          for (int j = 0; j < MT; ++j) MM::run(o[j][nt], a[j], b.x, b.y);
+          for (int part = PARTS - 1; part >= 0; --part) {
+            const uint2 b =
+                *reinterpret_cast<const uint2 *>(p_in + u * P_BLOCK + (part * NT + nt) * 256);
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+              if constexpr (F32) {
+                if (u == 0 && part == PARTS - 1) mma_first(part_sum[j][nt], a[j], b.x, b.y);
+                else MM::run(part_sum[j][nt], a[j], b.x, b.y);
+              } else {
+                MM::run(o[j][nt], a[j], b.x, b.y);
+              }
+            }
+          }
         }
+      }
+      if constexpr (F32) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < MT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[j][nt][e] += part_sum[j][nt][e];
       }
     }
 
@@ -494,9 +541,11 @@ __global__ void __launch_bounds__(kWarps * 32, (CtaShape<D, NT>::kMinCtas))
           T *dst = static_cast<T *>(p.out) + row * D + dim0;
           const float os = inv * p.out_scale;
 #pragma unroll
-          for (int j = 0; j < MT; ++j)
-            reinterpret_cast<uint32_t *>(dst)[j] =
-                Mma<T>::pack(o[j][nt][e] * os, o[j][nt][e + 2] * os);
+          for (int j = 0; j < MT; ++j) {
+            const float x = o[j][nt][e] * os, y = o[j][nt][e + 2] * os;
+            if constexpr (F32) reinterpret_cast<float2 *>(dst)[j] = make_float2(x, y);
+            else reinterpret_cast<uint32_t *>(dst)[j] = Mma<T>::pack(x, y);
+          }
         } else {
           const int64_t at = p.split_target == 0
                                  ? row * p.num_splits + cur.split
@@ -527,17 +576,17 @@ __global__ void __launch_bounds__(kWarps * 32, (CtaShape<D, NT>::kMinCtas))
   }
 }
 
-template <int D, int NT> constexpr size_t cta_smem() {
-  using SH = CtaShape<D, NT>;
+template <typename T, int D, int NT> constexpr size_t cta_smem() {
+  using SH = CtaShape<T, D, NT>;
   constexpr size_t stages = size_t(SH::NS) * SH::kGroup * 2 * Tile<D>::kBytes;
-  return stages + size_t(D / 16) * NT * 256 + size_t(2) * SH::kGroup * NT * 256 + 128;
+  return stages + size_t(SH::kParts) * NT * 256 * (D / 16 + 2 * SH::kGroup) + 128;
 }
 
 using Launch = cudaError_t (*)(const AttnParams &, dim3, cudaStream_t);
 
 template <typename T, int D, int NT>
 cudaError_t launch_t(const AttnParams &p, dim3 grid, cudaStream_t stream) {
-  return launch_kernel(true, cta_kernel<T, D, NT>, grid, kWarps * 32, cta_smem<D, NT>(), stream,
+  return launch_kernel(true, cta_kernel<T, D, NT>, grid, kWarps * 32, cta_smem<T, D, NT>(), stream,
                        p);
 }
 
@@ -545,10 +594,10 @@ template <typename T, int D, int NT> bool take(KernelInfo *info, Launch *launch)
   info->func = reinterpret_cast<const void *>(&cta_kernel<T, D, NT>);
   info->threads = kWarps * 32;
   info->warps = kWarps;
-  info->stages = CtaShape<D, NT>::NS;
-  info->smem = cta_smem<D, NT>();
+  info->stages = CtaShape<T, D, NT>::NS;
+  info->smem = cta_smem<T, D, NT>();
   info->warp_tiles = NT;
-  info->blocks_per_iter = CtaShape<D, NT>::kGroup;
+  info->blocks_per_iter = CtaShape<T, D, NT>::kGroup;
   *launch = &launch_t<T, D, NT>;
   return true;
 }
@@ -556,7 +605,15 @@ template <typename T, int D, int NT> bool take(KernelInfo *info, Launch *launch)
 // Tiles built: 1 to 6 and 8 at head_dim <= 128, 1, 2 and 4 at 256; another
 // number takes the next one.
 template <typename T, int D> bool pick_nt(int nt, KernelInfo *info, Launch *launch) {
-  if constexpr (D == 256) {
+  if constexpr (std::is_same<T, float>::value && D <= 128) {
+    return nt == 1   ? take<T, D, 1>(info, launch)
+           : nt == 2 ? take<T, D, 2>(info, launch)
+           : nt == 3 ? take<T, D, 3>(info, launch)
+           : nt == 4 ? take<T, D, 4>(info, launch)
+                     : false;
+  } else if constexpr (std::is_same<T, float>::value) {
+    return nt == 1 ? take<T, D, 1>(info, launch) : nt == 2 && take<T, D, 2>(info, launch);
+  } else if constexpr (D == 256) {
     return nt == 1   ? take<T, D, 1>(info, launch)
            : nt == 2 ? take<T, D, 2>(info, launch)
            : nt <= 4 ? take<T, D, 4>(info, launch)
@@ -589,6 +646,7 @@ bool pick(pkv_dtype q_dtype, int D, int nt, KernelInfo *info, Launch *launch) {
   switch (q_dtype) {
     case PKV_BF16: return pick_d<__nv_bfloat16>(D, nt, info, launch);
     case PKV_F16: return pick_d<__half>(D, nt, info, launch);
+    case PKV_F32: return pick_d<float>(D, nt, info, launch);
     default: return false;
   }
 }
@@ -596,7 +654,10 @@ bool pick(pkv_dtype q_dtype, int D, int nt, KernelInfo *info, Launch *launch) {
 }  // namespace
 }  // namespace fp4
 
-int cta_fp4_max_tiles(int head_dim) { return head_dim <= 128 ? 8 : 4; }
+int cta_fp4_max_tiles(pkv_dtype q_dtype, int head_dim) {
+  const int most = q_dtype == PKV_F32 ? 4 : 8;
+  return head_dim <= 128 ? most : most / 2;
+}
 
 bool cta_fp4_kernel_info(pkv_dtype q_dtype, int head_dim, int tiles, KernelInfo *info) {
   fp4::Launch launch = nullptr;

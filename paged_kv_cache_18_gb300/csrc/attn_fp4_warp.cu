@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kWarps * 32, (WarpShape<D, NT>::kMinCtas))
         if (r == 2 * c + 1) colfac[nt][1] = fac;
       }
     }
-    auto q_frag = [&](int ks, int nt, uint32_t &b0, uint32_t &b1) {
+    auto q_frag = [&](int ks, int nt, int, uint32_t &b0, uint32_t &b1) {
       b0 = qf[ks][nt][0];
       b1 = qf[ks][nt][1];
     };

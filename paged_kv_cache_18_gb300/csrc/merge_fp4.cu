@@ -147,6 +147,7 @@ cudaError_t merge_fp4_launch(pkv_dtype dtype, int head_dim, const AttnParams &p,
   switch (dtype) {
     case PKV_BF16: return fp4::merge_d<__nv_bfloat16>(head_dim, p, sm_count, stream);
     case PKV_F16: return fp4::merge_d<__half>(head_dim, p, sm_count, stream);
+    case PKV_F32: return fp4::merge_d<float>(head_dim, p, sm_count, stream);
     default: return cudaErrorInvalidValue;
   }
 }

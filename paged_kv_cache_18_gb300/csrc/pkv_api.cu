@@ -174,7 +174,8 @@ bool fp4_balanced(const Shape &s, const pkv_options *opt, int64_t units) {
 // warps.
 bool fp4_warp_workers(const Shape &s, const pkv_options *opt, int row_chunks, int rows) {
   const int64_t units = static_cast<int64_t>(s.batch) * s.num_kv_heads * row_chunks;
-  return fp4_balanced(s, opt, units) && rows <= 8 * warp_fp4_max_tiles(s.head_dim);
+  return s.qdtype != PKV_F32 && fp4_balanced(s, opt, units) &&
+         rows <= 8 * warp_fp4_max_tiles(s.head_dim);
 }
 
 // The same for a 4-bit cache.
@@ -184,11 +185,10 @@ bool choose_fp4_kernel(const Shape &s, const pkv_options *opt, int rows, pkv_pla
   if (opt && (opt->stages || opt->warp_tiles || opt->blocks_per_iter || opt->persistent ||
               opt->merge == 1))
     return false;  // (splits are merged by the merge kernel)
-  const bool f32 = s.qdtype == PKV_F32;  // no exact tensor-core path
-  if (kernel == PKV_KERNEL_AUTO) kernel = f32 ? PKV_KERNEL_SIMT : PKV_KERNEL_MMA;
-  if (kernel != PKV_KERNEL_SIMT && (kernel != PKV_KERNEL_MMA || f32)) return false;
+  if (kernel == PKV_KERNEL_AUTO) kernel = PKV_KERNEL_MMA;
+  if (kernel != PKV_KERNEL_SIMT && kernel != PKV_KERNEL_MMA) return false;
   const bool mma = kernel == PKV_KERNEL_MMA;
-  int cap = mma ? 8 * cta_fp4_max_tiles(s.head_dim) : simt_fp4_max_rows();
+  int cap = mma ? 8 * cta_fp4_max_tiles(s.qdtype, s.head_dim) : simt_fp4_max_rows();
   if (opt && opt->rows_per_cta > 0 && opt->rows_per_cta < cap) cap = opt->rows_per_cta;
   const int chunks = ceil_div(rows, cap);
   const int per_cta = ceil_div(rows, chunks);
@@ -933,9 +933,10 @@ pkv_status pkv_attention_workspace_size(int batch, int num_queries, int num_head
                                            block_size, max_context_len, dtype, options, &pl);
   if (st != PKV_OK) return st;
   *bytes = pl.workspace_bytes;
-  if (coded(dtype) && (!options || options->kernel != PKV_KERNEL_MMA)) {
-    // float32 queries over a cache of codes take the CUDA-core kernel: report
-    // enough for either plan.
+  if (dtype == PKV_FP4_E2M1 ||
+      (dtype == PKV_FP8_E4M3 && (!options || options->kernel != PKV_KERNEL_MMA))) {
+    // float32 queries over a cache of codes have a plan of their own: report
+    // enough for either.
     Shape s = make_shape(batch, num_queries, num_heads, num_kv_heads, head_dim, block_size,
                          max_context_len, dtype);
     s.qdtype = PKV_F32;

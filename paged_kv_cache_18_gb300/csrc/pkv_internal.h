@@ -115,11 +115,11 @@ bool simt_fp4_kernel_info(pkv_dtype q_dtype, int head_dim, int rows, KernelInfo 
 cudaError_t simt_fp4_launch(pkv_dtype q_dtype, int head_dim, int rows, const AttnParams &p,
                             dim3 grid, cudaStream_t stream);
 
-// Tensor-core attention over a 4-bit cache: bf16 / f16 q, `tiles` 8-column tiles
+// Tensor-core attention over a 4-bit cache: `tiles` 8-column tiles
 // of query rows per worker.  Workers are CTAs (attn_fp4_cta.cu: every split
-// plan) or warps (attn_fp4_warp.cu: the balanced partition with p.split_target =
-// 4 times the grid).
-int cta_fp4_max_tiles(int head_dim);
+// plan) or warps (attn_fp4_warp.cu: 16-bit q, the balanced partition with
+// p.split_target = 4 times the grid).
+int cta_fp4_max_tiles(pkv_dtype q_dtype, int head_dim);
 bool cta_fp4_kernel_info(pkv_dtype q_dtype, int head_dim, int tiles, KernelInfo *info);
 cudaError_t cta_fp4_launch(pkv_dtype q_dtype, int head_dim, int tiles, const AttnParams &p,
                            dim3 grid, cudaStream_t stream);

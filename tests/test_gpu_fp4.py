@@ -274,15 +274,17 @@ def test_row_chunks(kernel, rows):
 @pytest.mark.parametrize("Q,Hq,Hkv", [(2, 8, 2), (3, 8, 2), (5, 8, 2), (8, 8, 2), (10, 8, 2),
                                       (11, 8, 2), (13, 8, 2), (31, 4, 1), (64, 3, 1)])
 @pytest.mark.parametrize("split_blocks", [0, 5])
-def test_every_column_tile(D, Q, Hq, Hkv, split_blocks):
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_every_column_tile(dtype, D, Q, Hq, Hkv, split_blocks):
     lens = [Q, Q + 1, Q + 40, 333, 1200]
-    cap, built = (64, (1, 2, 3, 4, 5, 6, 8)) if D <= 128 else (32, (1, 2, 4))
-    rows = Q * Hq // Hkv
-    chunks = -(-rows // cap)
-    tiles = -(-(-(-rows // chunks)) // 8)
-    p = pkv.plan(len(lens), Q, Hq, Hkv, D, max(lens), "fp4", split_blocks=split_blocks)
-    assert p["row_chunks"] == chunks and p["warp_tiles"] == min(n for n in built if n >= tiles)
-    run(W.Workload("fp4 tiles", len(lens), Hq, Hkv, D, "bf16", context_lens=lens, num_queries=Q,
+    if dtype == "bf16":
+        cap, built = (64, (1, 2, 3, 4, 5, 6, 8)) if D <= 128 else (32, (1, 2, 4))
+        rows = Q * Hq // Hkv
+        chunks = -(-rows // cap)
+        tiles = -(-(-(-rows // chunks)) // 8)
+        p = pkv.plan(len(lens), Q, Hq, Hkv, D, max(lens), "fp4", split_blocks=split_blocks)
+        assert p["row_chunks"] == chunks and p["warp_tiles"] == min(n for n in built if n >= tiles)
+    run(W.Workload("fp4 tiles", len(lens), Hq, Hkv, D, dtype, context_lens=lens, num_queries=Q,
                    seed=2155 + Q), split_blocks=split_blocks)
 
 
@@ -320,10 +322,11 @@ def test_rows_that_see_nothing_are_zero(dtype):
     assert (got[0, 1] == 0).all() and (got[1, 1] != 0).any()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("kernel", [0, 1])
-def test_query_range(kernel):
+def test_query_range(kernel, dtype):
     gains = [3.0e4, 1.0e-6, 1.0, 2.0 ** 40, 2.0 ** -60, 0.0, 7.5, 1.0e8]
-    run(W.Workload("fp4 q range", 3, 8, 2, 128, "bf16", context_lens=[5, 64, 517], seed=2190),
+    run(W.Workload("fp4 q range", 3, 8, 2, 128, dtype, context_lens=[5, 64, 517], seed=2190),
         kernel=kernel, q_gain=gains)
 
 
@@ -334,9 +337,9 @@ def test_tensor_scales(k_scale, v_scale):
         k_scale=k_scale, v_scale=v_scale)
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("dtype,kernel", [("bf16", 0), ("f16", 0), ("f32", 0), ("f32", 1)])
 @pytest.mark.parametrize("Q,split_blocks", [(1, 0), (1, 100000), (5, 0)])
-def test_a_peak_over_a_long_flat_tail(dtype, Q, split_blocks):
+def test_a_peak_over_a_long_flat_tail(dtype, kernel, Q, split_blocks):
     # one key scores 20 bits above 40000 equal ones, which together weigh 5 % of
     # it: every weight of the tail has to keep its bits (rounded to a multiple of
     # 2^-24 of the peak each would be off by 3 %, the result by 1e-3)
@@ -356,14 +359,14 @@ def test_a_peak_over_a_long_flat_tail(dtype, Q, split_blocks):
                                   torch.from_numpy(kc).to(DEV), torch.from_numpy(vc).to(DEV),
                                   torch.from_numpy(table).to(DEV), torch.from_numpy(lens).to(DEV),
                                   1.0, 1.0, scale=scale, max_context_len=L,
-                                  split_blocks=split_blocks)
+                                  kernel=kernel, split_blocks=split_blocks)
     ref = fp4.attention(qt.float().numpy(), kc, vc, table, lens, scale, 1.0, 1.0)
     got = got.double().cpu().numpy().reshape(ref.shape)
     # the output's rounding, the exponentials' argument (20 bits at 2^-24 relative),
     # the float32 sums, and the weights' 2^-11 (the peak's own)
     tol = half_ulp(ref, dtype) + 20 * 2.0 ** -23
     if dtype == "f32":
-        # A warp adds every fourth block key by key.  Its running numerator is at most
+        # On CUDA cores a warp adds every fourth block key by key.  Its running numerator is at most
         # 0.5 + 0.013, so each of its L / 4 additions is off by at most 2^-25; its sum of
         # weights is below 2, and gets one addition a block, off by at most 2^-24.
         tol = tol + L / 4 * 2.0 ** -25 + L / 64 * 2.0 ** -24
