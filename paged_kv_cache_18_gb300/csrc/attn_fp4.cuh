@@ -277,7 +277,7 @@ constexpr int kMinPlaces = 16;  // of a worker
 
 // The pieces of work of a worker (a CTA or a warp), in turn: one under the
 // host's and the device's split partitions (cta_work), under the balanced one
-// the parts of units in its range of the list (sk_begin, pkv_device.cuh).
+// the parts of units in its range of the list of all places.
 // Warp-collective; the warps of a CTA that is a worker walk alike.
 struct Piece {
   int b, kvh, chunk, L;
@@ -335,8 +335,9 @@ struct Pieces {
     // the slots of a unit's pieces are consecutive.
     const int workers = min(p.split_target, max(total / kMinPlaces, 1));
     if (worker >= workers) return false;
-    x = static_cast<int>(sk_begin(total, workers, worker));
-    x1 = static_cast<int>(sk_begin(total, workers, worker + 1));
+    const int each = total / workers, more = total - each * workers;  // (32-bit divisions)
+    x = worker * each + min(worker, more);
+    x1 = x + each + (worker < more ? 1 : 0);
     base = from = 0;
     begin = nblk = 0;
     return next(p, w);

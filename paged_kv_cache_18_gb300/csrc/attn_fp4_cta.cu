@@ -323,10 +323,12 @@ __global__ void __launch_bounds__(kWarps * 32, (CtaShape<T, D, NT>::kMinCtas))
       }
       constexpr int UB = SH::UB;
       float sc[UW][NT][4];
+      if (UW == 1 || blk < nspan) {
 #pragma unroll
-      for (int u = 0; u < UW; u += UB)
-        block_scores<D, NT, UB, PARTS>(reinterpret_cast<float(&)[UB][NT][4]>(sc[u]), tile + u * PAIR, g, c,
-                                q_frag);
+        for (int u = 0; u < UW; u += UB)
+          block_scores<D, NT, UB, PARTS>(reinterpret_cast<float(&)[UB][NT][4]>(sc[u]),
+                                         tile + u * PAIR, g, c, q_frag);
+      }
       if (edge) {
         const int kk = key_of(g);
 #pragma unroll
@@ -417,7 +419,7 @@ __global__ void __launch_bounds__(kWarps * 32, (CtaShape<T, D, NT>::kMinCtas))
             float top = s_top[0][col];
 #pragma unroll
             for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_top[w][col]);
-            const float m_new = fmaxf(m[nt][e], top - kHead / fac[nt][e]);
+            const float m_new = fmaxf(m[nt][e], top - __fdividef(kHead, fac[nt][e]));
             const float corr = ex2((m[nt][e] - m_new) * fac[nt][e]);
             l[nt][e] *= corr;
             m[nt][e] = m_new;
@@ -443,8 +445,7 @@ __global__ void __launch_bounds__(kWarps * 32, (CtaShape<T, D, NT>::kMinCtas))
       // (float32: the group's products have a sum of their own, so that a long
       // context is not a long chain of the MMA's roundings)
       float part_sum[F32 ? MT : 1][F32 ? NT : 1][4];
-#pragma unroll
-      for (int u = 0; u < kGroup; ++u) {
+      auto add_block = [&](int u) {
         constexpr uint32_t LOW = 0x0f0f0f0fu;
         const uint4 w = lds128(stage + u * PAIR + v_off);
         const uint32_t sw = lds32(stage + u * PAIR + vs_off);
@@ -496,7 +497,14 @@ __global__ void __launch_bounds__(kWarps * 32, (CtaShape<T, D, NT>::kMinCtas))
             }
           }
         }
-      }
+      };
+#pragma unroll
+      for (int u = 0; u < 4; ++u) add_block(u);
+      if constexpr (kGroup == 8)
+        if (nspan - i * kGroup > 4) {  // (a piece's last group may be half empty)
+#pragma unroll
+          for (int u = 4; u < 8; ++u) add_block(u);
+        }
       if constexpr (F32) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)

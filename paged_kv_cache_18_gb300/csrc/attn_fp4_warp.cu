@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kWarps * 32, (WarpShape<D, NT>::kMinCtas))
             mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
-            const float m_new = fmaxf(m[nt][e], mx - kHead / colfac[nt][e]);
+            const float m_new = fmaxf(m[nt][e], mx - __fdividef(kHead, colfac[nt][e]));
             const float corr = ex2((m[nt][e] - m_new) * colfac[nt][e]);
             l[nt][e] *= corr;
             m[nt][e] = m_new;
