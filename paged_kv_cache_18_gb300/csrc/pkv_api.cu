@@ -35,11 +35,15 @@ constexpr int kMaxSplits = 32;          // per sequence: each split adds merge w
 // first chunk's scores, the epilogue: ~5 us against ~0.2 us a block on the
 // verify step).
 constexpr int kStreamKWeight = 24;
-// The same for the 4-bit cache's tensor-core kernel, its workers being CTAs or
-// warps, the fewest blocks worth a CTA, and the longest batch whose lengths
-// every worker adds up.
+// The same for the 4-bit cache's tensor-core kernels, whose workers are CTAs (the
+// ten-node tree 61.5 us at 16, 65.5 at 8, 63.5 at 32) or warps (GQA decode 64.7 us at
+// 8, 68.3 at 4, 66.8 at 16; 40-head decode 70.6, 70.6, 75.0); the fewest blocks worth
+// a CTA (one context of 5000 rows 9.3 us at 4, 10.8 at 16); the blocks from which
+// warps are the workers at head_dim 256 (fp4_warp_workers); and the longest batch
+// whose lengths every worker adds up.
 constexpr int kFp4Weight = 16, kFp4WarpWeight = 8;
-constexpr int kFp4MinBlocks = 16;
+constexpr int kFp4MinBlocks = 4;
+constexpr int kFp4WarpBlocks = 16384;
 constexpr int kFp4MaxBatch = 1024;
 constexpr size_t kUsableSmemPerSm = 228 * 1024;
 
@@ -165,17 +169,23 @@ pkv_status check_shape(const Shape &s) {
 // on the device).
 bool fp4_balanced(const Shape &s, const pkv_options *opt, int64_t units) {
   const int max_blocks = ceil_div(s.max_context_len, s.block_size);
-  return !(opt && (opt->split_blocks > 0 || opt->split_waves != 0)) && s.batch <= kFp4MaxBatch && max_blocks > kMinSplitBlocks &&
+  return !(opt && (opt->split_blocks > 0 || opt->split_waves != 0)) &&
+         s.batch <= kFp4MaxBatch && max_blocks > kMinSplitBlocks &&
          units * (max_blocks + kFp4Weight) < (int64_t(1) << 31);
 }
 
 // With up to 16 query rows (8 at head_dim 256) each warp is a worker of the
 // balanced partition: a piece costs a warp its start and end once instead of four
-// warps.
+// warps (40-head decode 70.5 us, CTAs 106.8; 16 rows of 64 contexts of 2000 rows
+// 51.7 and 62.0; with 24 rows CTAs win, 30.2 against 38.4).  Warps at head_dim 256
+// want blocks enough for each (64 contexts of 1500 rows 31.9 us, CTAs 37.0; 16 of 500
+// to 3000 24.0, CTAs 20.0: 24064 and 12032 blocks).
 bool fp4_warp_workers(const Shape &s, const pkv_options *opt, int row_chunks, int rows) {
   const int64_t units = static_cast<int64_t>(s.batch) * s.num_kv_heads * row_chunks;
+  const int64_t blocks = units * ceil_div(s.max_context_len, s.block_size);
   return s.qdtype != PKV_F32 && fp4_balanced(s, opt, units) &&
-         rows <= 8 * warp_fp4_max_tiles(s.head_dim);
+         rows <= 8 * warp_fp4_max_tiles(s.head_dim) &&
+         (s.head_dim <= 128 || blocks >= kFp4WarpBlocks);
 }
 
 // The same for a 4-bit cache.

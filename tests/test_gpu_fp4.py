@@ -288,6 +288,16 @@ def test_every_column_tile(dtype, D, Q, Hq, Hkv, split_blocks):
                    seed=2155 + Q), split_blocks=split_blocks)
 
 
+@pytest.mark.parametrize("Q,Hq", [(1, 8), (2, 32)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_many_units_at_head_dim_256(dtype, Q, Hq):
+    lens = [Q + n for n in [0, 14, 15, 16, 31, 32, 33, 400, 1100, 780] * 4]
+    p = pkv.plan(len(lens), Q, Hq, 8, 256, max(lens), "fp4")
+    assert p["split_target"] == 4 * p["grid_x"]  # (warps are the workers)
+    run(W.Workload("fp4 units", len(lens), Hq, 8, 256, dtype, context_lens=lens, num_queries=Q,
+                   seed=2158 + Q))
+
+
 @pytest.mark.parametrize("kernel", [0, 1])
 @pytest.mark.parametrize("D,Q,dtype", [(128, 1, "bf16"), (64, 3, "f16"), (256, 2, "f32")])
 def test_partition_from_the_real_lengths(kernel, D, Q, dtype):
