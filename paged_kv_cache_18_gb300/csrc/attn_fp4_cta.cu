@@ -1,25 +1,30 @@
 // attn_fp4_cta.cu -- attention over the block-scaled 4-bit cache (fp4.cuh) on
-// tensor cores, a CTA being the worker: every split plan, few units, and up to
-// 64 query rows in one pass.  q and out bfloat16 or float16.
+// tensor cores, a CTA being the worker: every split plan, float32 queries, and up
+// to 64 query rows in one pass (32 at head_dim 256; float32: half as many).
 //
-// Per group of eight blocks (128 keys), keys on the MMA's M side and NT tiles of
+// Per group of 4 UW blocks (UW = 2 or 1), keys on the MMA's M side and NT tiles of
 // 8 query columns on N:
-//   warp w       S^T = K Q^T of blocks 2w, 2w + 1, their softmax weights P^T (online
+//   warp w       S^T = K Q^T of its UW blocks, their softmax weights P^T (online
 //                softmax, log2 units), which go to shared memory as operand
 //                fragments;
 //   one barrier
-//   every warp   O^T += V^T P^T over all eight blocks, for its quarter of the dims.
+//   every warp   O^T += V^T P^T over all the group's blocks, for its quarter of the
+//                dims.
 // So every code is widened once in the CTA, and a warp's O^T is D / 64 m-tiles
 // high: with 40 rows 40 registers a lane instead of 160, which leaves room for
 // the warps that hide the conversions behind the MMAs of others.  (With a warp
-// computing whole blocks for all columns, 20 and 40 rows ran at 0.30 and 0.15
-// of the bytes' floor.)  P^T is double-buffered and the reference of the online
-// softmax is the CTA's, so the fast path needs no second barrier.
+// computing whole blocks for all columns, 20 and 40 rows took 51 and 90 us on the
+// steps below.)  P^T is double-buffered and the reference of the online softmax is
+// the CTA's, so the fast path needs no second barrier.
 //
 // Codes are widened to f16 pairs by the conversion unit and multiplied by
 // their block scale there: code * scale has at most 6 significant bits, so the
-// operands are exact; q enters as f16 (convert_row), the weights as f16 (2^-11
-// relative, below the output's own rounding); sums are float32.
+// operands are exact; 16-bit q enters as f16 (convert_row), the weights as f16
+// (2^-11 relative, below the output's own rounding); sums are float32.  A float32
+// q row and its weights enter as sums of three f16 parts (33 bits, so 24 survive),
+// three MMAs for one; the small parts of the scores, and each group's P.V, have a
+// float32 sum of their own, the MMA's sums being rounded less well than float32's.
+// Against the CUDA-core kernel: GQA decode 267 -> 78 us, a ten-node tree 654 -> 137.
 //
 // The order of keys and dims inside the MMAs is free, and chosen so that no
 // operand is shuffled between lanes: lane (g, c) = (lane / 4, lane % 4) of the
@@ -27,6 +32,14 @@
 // then leaves it the weights of keys 4c .. 4c + 3 of a column; for P.V it reads
 // those keys' codes of its D / 32 dims, and a nibble merge pairs two keys' codes
 // of a dim in one byte, which converts to one operand register.
+//
+// What bounds it (D = 128, 16 sequences of 512 to 8192 rows, 8 KV heads, 81 MB): a
+// block costs an SM 116 ns with 20 rows (41 us for the step) and 175 ns with 40
+// (61 us), where its bytes take 52.  That is the time of its MMAs (16 a tile; one
+// every two clocks) and of issuing the other instructions (370 and 560), added up:
+// two or three CTAs an SM, one or two blocks a warp and group, rings of two to four
+// groups all come within 2 %.  About 14 us a call are outside that loop: the
+// first loads' chain, a piece's start and end, the merge.
 #include "attn_fp4.cuh"
 
 namespace pkv {
@@ -36,11 +49,14 @@ namespace {
 template <typename T, int D, int NT> struct CtaShape {
   static constexpr bool kF32 = std::is_same<T, float>::value;
   static constexpr int kParts = kF32 ? 3 : 1;  // f16 parts of a query element and a weight
-  static constexpr int UW = NT <= (kF32 ? 2 : 4) ? 2 : 1;  // blocks of a group that are a warp's
+  // Blocks of a group that are a warp's: two, while their scores fit in registers
+  // (20 rows 41.0 us, with one 42.6; 40 rows 61.7 both ways).
+  static constexpr int UW = NT <= (kF32 ? 2 : 4) ? 2 : 1;
   static constexpr int kGroup = UW * kWarps;               // blocks of a group
   static constexpr int NS = UW == 2 ? 2 : 4;               // groups in the ring
   static constexpr bool kRegQ = NT <= 2 && D <= 128 && !kF32;  // Q^T fragments in registers
-  // blocks whose scores are computed together, each Q^T fragment loaded once
+  // Blocks whose scores are computed together, each Q^T fragment loaded once (20
+  // rows 41.0 us, one at a time 44.3).
   static constexpr int UB = !kRegQ && NT <= 4 && D <= 128 && !kF32 ? UW : 1;
   static constexpr bool kRegFac = NT <= 4;    // score factors in registers
   // resident CTAs it is compiled for
@@ -610,8 +626,9 @@ template <typename T, int D, int NT> bool take(KernelInfo *info, Launch *launch)
   return true;
 }
 
-// Tiles built: 1 to 6 and 8 at head_dim <= 128, 1, 2 and 4 at 256; another
-// number takes the next one.
+// Tiles built: 1 to 6 and 8 at head_dim <= 128, 1, 2 and 4 at 256 (float32: 1 to 4,
+// 1 and 2); another number takes the next one.  float32: 32 rows in one pass 95.6
+// us, in two of 16 rows 100.
 template <typename T, int D> bool pick_nt(int nt, KernelInfo *info, Launch *launch) {
   if constexpr (std::is_same<T, float>::value && D <= 128) {
     return nt == 1   ? take<T, D, 1>(info, launch)

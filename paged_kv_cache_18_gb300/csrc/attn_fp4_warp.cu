@@ -1,23 +1,28 @@
 // attn_fp4_warp.cu -- attention over the block-scaled 4-bit cache (fp4.cuh) on
-// tensor cores, a warp being the worker: many units (sequence, KV head, row
-// chunk) of up to 16 query rows.  q and out bfloat16 or float16.
+// tensor cores, a warp being the worker: up to 16 query rows (8 at head_dim 256) a
+// unit (sequence, KV head, row chunk).  q and out bfloat16 or float16.
 //
 // Each resident warp takes an equal share of the batch's blocks (the balanced
 // partition) on its own: no barrier, no partner.  Against a CTA as the worker
 // (attn_fp4_cta.cu) a piece costs its start and end once instead of four times,
-// and a block its conversions only: 40-head decode 88 -> 74 us, GQA 87 -> 68 us.
+// and nothing goes through shared memory but the copies: 40-head decode 70.5 us,
+// CTAs 106.8; 2 contexts of 32768 and 65536 rows 29.7 and 38.0.
 // Per group of KB blocks, keys on the MMA's M side and NT tiles of 8 query
 // columns on N:
 //   S^T = K Q^T,  online softmax over the keys (log2 units),  O^T += V^T P^T.
 // The operands are those of the CTA kernel; for P.V a lane reads four keys' codes
 // of 8 dims (word g + 8 h of the tile): 16 bytes.
 //
-// What bounds it: the 40-head decode step (377 MB of codes and scales) spends 55
-// ns a block and SM in this loop, 6.4 TB/s; per block 64 conversions, 64 f16
-// multiplies, 16 MMAs and about 110 other instructions.  Groups of four blocks
-// share a wait, a vote and the copies' issue (one block: 96 us, two: 83 us, four:
-// 77 us in an earlier form); two groups of four a ring (18 KB a warp, 12 warps an
-// SM) hold more bytes in flight than the latency needs.
+// What bounds it: the 40-head decode step (32 contexts of 2048 rows, 377 MB of codes
+// and scales) takes 70.5 us, 0.79 of the copy bandwidth: its loop spends 53 ns a
+// block and SM where the bytes take 52, the rest is the call's start, the pieces'
+// ends and the merge.  Per block 64 conversions, 64 f16 multiplies, 16 MMAs and
+// about 110 other instructions.  Groups of four blocks share a wait, a vote and the
+// copies' issue (one block: 96 us, two: 83 us, four: 77 us in an earlier form); two
+// groups of four a ring (18 KB a warp, 12 warps an SM) hold more bytes in flight
+// than the latency needs.  With two tiles groups of two leave registers to spare (16
+// rows of 64 contexts of 2000 rows 51.7 us, groups of four 54.4), as they do at
+// head_dim 256 (64 contexts of 1500 rows 31.9 us, one block 33.3).
 #include "attn_fp4.cuh"
 
 namespace pkv {

