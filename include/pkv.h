@@ -458,7 +458,8 @@ PKV_API pkv_status pkv_paged_attention_fp8(
  * rounded to nearest even and saturating (s at 448, codes at 6).  A block whose
  * s is 0 is stored as zeros; one that holds a NaN gets a NaN scale and codes 0.
  * k_new, v_new: [num_tokens, num_kv_heads, head_dim] of src_dtype
- * (F32/BF16/F16); slots and errors as for pkv_kv_append.
+ * (F32/BF16/F16); slots and errors as for pkv_kv_append (a slot named twice is
+ * left with codes and scales of either row).
  */
 PKV_API pkv_status pkv_kv_append_fp4(const void *k_new, const void *v_new, void *k_cache,
                                      void *v_cache, const int64_t *slot_mapping,
@@ -490,9 +491,13 @@ PKV_API pkv_status pkv_kv_load_fp4(void *k_out, void *v_out, const void *k_cache
  * num_queries, num_heads, head_dim]; tree_mask and mask_batch_stride as for
  * pkv_tree_verify_attention (NULL, 0: causal).  Plans and workspace sizes: the
  * plan and workspace functions with dtype PKV_FP4_E2M1 (the plan is the one for
- * 16-bit q; the workspace size covers float32 q too).  options: kernel,
- * split_blocks, rows_per_cta and split_waves (merge 0 or 2); the others must
- * be 0.
+ * 16-bit q; the workspace size covers float32 q too).  A workspace serves one call
+ * at a time: calls on several streams, and captured graphs that may run at the same
+ * time, need one each.  options: kernel, split_blocks, rows_per_cta and split_waves
+ * (merge 0 or 2); the others must be 0.  kernel 0 and PKV_KERNEL_MMA use tensor cores
+ * for every q_dtype: F32 q (and its softmax weights) in three f16 parts after a shift
+ * by a power of two, which keeps 24 bits of an element down to 2^-14 of its row's
+ * largest and 2^-39 of that largest below; PKV_KERNEL_SIMT sums in plain float32.
  */
 PKV_API pkv_status pkv_paged_attention_fp4(
     void *out, const void *q, const void *k_cache, const void *v_cache,
@@ -520,7 +525,7 @@ PKV_API pkv_status pkv_paged_attention_fp4(
  *                  max_path and num_queries <= 64
  *   path_lens    : device int32 [batch], 0 <= n_b <= min(max_path, num_queries)
  *   new_lens     : NULL, or device int32 [batch]: the new lengths; must not
- *                  overlap context_lens
+ *                  overlap context_lens, path, path_lens or block_table
  * The moved rows must be in blocks that no other sequence of the batch uses
  * (copy-on-write first).  A sequence whose path breaks its rules, or whose
  * length is below num_queries or past the table, keeps its rows and length and

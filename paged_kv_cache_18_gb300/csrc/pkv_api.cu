@@ -1334,10 +1334,16 @@ pkv_status pkv_commit_rows(void *const *k_caches, void *const *v_caches, int num
   if (!aligned(block_table, 4) || !aligned(context_lens, 4) || !aligned(path, 4) ||
       !aligned(path_lens, 4) || !aligned(new_lens, 4) || !aligned(error_word, 4))
     return PKV_ERR_ALIGNMENT;
-  // the lengths are read by every warp and written by one
-  const uintptr_t a = reinterpret_cast<uintptr_t>(new_lens),
-                  c = reinterpret_cast<uintptr_t>(context_lens), len = 4 * uintptr_t(batch);
-  if (new_lens && a < c + len && c < a + len) return PKV_ERR_INVALID_ARG;
+  // the lengths, paths and table are read by every warp, the new lengths written by one
+  auto meets = [&](const void *other, uint64_t entries) {
+    const uintptr_t w = reinterpret_cast<uintptr_t>(new_lens),
+                    r = reinterpret_cast<uintptr_t>(other);
+    return w < r + 4 * entries && r < w + 4 * uintptr_t(batch);
+  };
+  if (new_lens && (meets(context_lens, batch) || meets(path_lens, batch) ||
+                   meets(path, uint64_t(batch) * max_path) ||
+                   meets(block_table, uint64_t(batch) * max_blocks_per_seq)))
+    return PKV_ERR_INVALID_ARG;
   // Every tensor once: a second move of the same rows would find them moved.
   const int tensors = v_caches ? 2 * num_layers : num_layers;
   const uint64_t cache_bytes =

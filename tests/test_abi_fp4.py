@@ -126,6 +126,8 @@ def commit(L, **kw):
     (dict(path=2), 5), (dict(new=2), 5), (dict(err=3), 5),
     (dict(k=(4096, None)), 1), (dict(k=(4096, (1 << 20) + 8)), 5),
     (dict(new=1024), 1), (dict(new=1028), 1),                    # overlaps the lengths
+    (dict(table=8192, new=8192 + 4 * 15), 1), (dict(path=8192, new=8192 + 20), 1),
+    (dict(path_lens=8192, new=8196), 1),                         # or what else every warp reads
     (dict(k=(4096, 4096)), 1), (dict(v=(2 << 20, 4096)), 1),     # a tensor named twice
     (dict(k=(4096, 4096 + 10 * 2 * 16 * 64 * 2 - 16)), 1)])      # two that overlap
 def test_commit_argument_errors(L, kw, status):
