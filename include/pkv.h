@@ -495,9 +495,9 @@ PKV_API pkv_status pkv_kv_load_fp4(void *k_out, void *v_out, const void *k_cache
  * at a time: calls on several streams, and captured graphs that may run at the same
  * time, need one each.  options: kernel, split_blocks, rows_per_cta and split_waves
  * (merge 0 or 2); the others must be 0.  kernel 0 and PKV_KERNEL_MMA use tensor cores
- * for every q_dtype: F32 q (and its softmax weights) in three f16 parts after a shift
- * by a power of two, which keeps 24 bits of an element down to 2^-14 of its row's
- * largest and 2^-39 of that largest below; PKV_KERNEL_SIMT sums in plain float32.
+ * for every q_dtype: F32 q (and its softmax weights) in two f16 parts after a shift by
+ * a power of two, an element being off by at most 2^-24 of itself or 2^-39 of its
+ * row's largest; PKV_KERNEL_SIMT sums in plain float32.
  */
 PKV_API pkv_status pkv_paged_attention_fp4(
     void *out, const void *q, const void *k_cache, const void *v_cache,

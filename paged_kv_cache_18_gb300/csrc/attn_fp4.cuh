@@ -80,7 +80,7 @@ __device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4],
 // Scores of UB blocks that lie one after another (key tile, value tile) from
 // shared address `blk`: S^T[16 keys x 8 NT] = K Q^T of each; `q(ks, nt, part, b0, b1)`
 // gives the Q^T fragment of a k-step and tile.  Queries in PARTS f16 parts
-// (split_row): the products with the small parts have a sum of their own, so that
+// (split_row): the products with the small part have a sum of their own, so that
 // the large one sees as few roundings as with one part.
 // Lane (g, c) reads 32 dims of each panel of its two keys; k-step (panel, word w,
 // half e) holds dims  panel + 8 WP c + 8 w + 4 e + {0, 1 | 2, 3}.
@@ -217,26 +217,27 @@ __device__ __forceinline__ float convert_row(uint32_t (&f)[WORDS], float scale_l
   }
 }
 
-// Two float32 values as three f16 pairs: x = hi + mid + lo, to 2^-25 absolute.  An
+// float32 operands enter the f16 MMAs as two parts.
+constexpr int kF32Parts = 2;
+
+// Two float32 values as two f16 pairs: x = hi + lo to 2^-24 of x -- lo rounds what is
+// left, at most 2^-12 of x, to 2^-12 of that -- or 2^-25 where lo is subnormal.  An
 // infinity or NaN is the first part's alone.
-__device__ __forceinline__ void split_pair(float x, float y, uint32_t (&part)[3]) {
-#pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    part[k] = Mma<__half>::pack(x, y);
-    float hx, hy;
-    Mma<__half>::unpack(part[k], hx, hy);
-    x = isfinite(x) ? x - hx : 0.f;  // (exact)
-    y = isfinite(y) ? y - hy : 0.f;
-  }
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t (&part)[kF32Parts]) {
+  part[0] = Mma<__half>::pack(x, y);
+  float hx, hy;
+  Mma<__half>::unpack(part[0], hx, hy);
+  part[1] = Mma<__half>::pack(isfinite(x) ? x - hx : 0.f, isfinite(y) ? y - hy : 0.f);
 }
 
-// A float32 query row as f16 operands in three parts: shifted by a power of two so
-// that its largest magnitude lies in [2^14, 2^15), an element keeps its 24 bits
-// down to 2^-14 of the largest and is off by 2^-39 of that below.  Returns the row's
-// score factor (convert_row).  Warp-collective.
+// A float32 query row as f16 operands in two parts: shifted by a power of two so that
+// its largest magnitude lies in [2^14, 2^15), an element is off by at most 2^-24 of
+// itself or 2^-39 of the largest.  Returns the row's score factor (convert_row).
+// Warp-collective.
 template <int PER>
 __device__ __forceinline__ float split_row(const uint32_t (&f)[PER],
-                                           uint32_t (&parts)[3][PER / 2], float scale_log2) {
+                                           uint32_t (&parts)[kF32Parts][PER / 2],
+                                           float scale_log2) {
   uint32_t top = 0;
 #pragma unroll
   for (int k = 0; k < PER; ++k) top = max(top, f[k] & 0x7fffffffu);
@@ -246,10 +247,10 @@ __device__ __forceinline__ float split_row(const uint32_t (&f)[PER],
   const float up = __int_as_float((127 + qshift) << 23);
 #pragma unroll
   for (int k = 0; k < PER; k += 2) {
-    uint32_t part[3];
+    uint32_t part[kF32Parts];
     split_pair(__uint_as_float(f[k]) * up, __uint_as_float(f[k + 1]) * up, part);
 #pragma unroll
-    for (int j = 0; j < 3; ++j) parts[j][k / 2] = part[j];
+    for (int j = 0; j < kF32Parts; ++j) parts[j][k / 2] = part[j];
   }
   return fminf(fmaxf(scale_log2 * __int_as_float((127 - qshift) << 23), kTiny), kHuge);
 }

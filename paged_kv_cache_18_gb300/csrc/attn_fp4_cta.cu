@@ -1,6 +1,6 @@
 // attn_fp4_cta.cu -- attention over the block-scaled 4-bit cache (fp4.cuh) on
 // tensor cores, a CTA being the worker: every split plan, float32 queries, and up
-// to 64 query rows in one pass (32 at head_dim 256; float32: half as many).
+// to 64 query rows in one pass (32 at head_dim 256; float32: 48 and 16).
 //
 // Per group of 4 UW blocks (UW = 2 or 1), keys on the MMA's M side and NT tiles of
 // 8 query columns on N:
@@ -21,10 +21,11 @@
 // their block scale there: code * scale has at most 6 significant bits, so the
 // operands are exact; 16-bit q enters as f16 (convert_row), the weights as f16
 // (2^-11 relative, below the output's own rounding); sums are float32.  A float32
-// q row and its weights enter as sums of three f16 parts (33 bits, so 24 survive),
-// three MMAs for one; the small parts of the scores, and each group's P.V, have a
-// float32 sum of their own, the MMA's sums being rounded less well than float32's.
-// Against the CUDA-core kernel: GQA decode 267 -> 78 us, a ten-node tree 654 -> 137.
+// q row and its weights enter as sums of two f16 parts (split_pair: to 2^-24, what
+// float32 itself rounds by), two MMAs for one; the small part of the scores, and each
+// group's P.V, have a float32 sum of their own, the MMA's sums being rounded less
+// well than float32's.  Against the CUDA-core kernel: GQA decode 267 -> 69 us, a ten-node
+// tree 654 -> 85 (with three parts 78 and 137).
 //
 // The order of keys and dims inside the MMAs is free, and chosen so that no
 // operand is shuffled between lanes: lane (g, c) = (lane / 4, lane % 4) of the
@@ -48,19 +49,20 @@ namespace {
 
 template <typename T, int D, int NT> struct CtaShape {
   static constexpr bool kF32 = std::is_same<T, float>::value;
-  static constexpr int kParts = kF32 ? 3 : 1;  // f16 parts of a query element and a weight
+  static constexpr int kParts = kF32 ? kF32Parts : 1;  // f16 parts of a query element, a weight
   // Blocks of a group that are a warp's: two, while their scores fit in registers
-  // (20 rows 41.0 us, with one 42.6; 40 rows 61.7 both ways).
+  // (20 rows 41.0 us, with one 42.6; 40 rows 61.7 both ways; float32, 20 rows, two
+  // CTAs an SM with two 42.5, three with one 41.5).
   static constexpr int UW = NT <= (kF32 ? 2 : 4) ? 2 : 1;
   static constexpr int kGroup = UW * kWarps;               // blocks of a group
   static constexpr int NS = UW == 2 ? 2 : 4;               // groups in the ring
   static constexpr bool kRegQ = NT <= 2 && D <= 128 && !kF32;  // Q^T fragments in registers
   // Blocks whose scores are computed together, each Q^T fragment loaded once (20
   // rows 41.0 us, one at a time 44.3).
-  static constexpr int UB = !kRegQ && NT <= 4 && D <= 128 && !kF32 ? UW : 1;
+  static constexpr int UB = !kRegQ && NT <= 4 && D <= 128 ? UW : 1;
   static constexpr bool kRegFac = NT <= 4;    // score factors in registers
   // resident CTAs it is compiled for
-  static constexpr int kMinCtas = D == 256 ? 1 : (NT >= (kF32 ? 3 : 6) ? 2 : 3);
+  static constexpr int kMinCtas = D == 256 ? 1 : (NT >= (kF32 ? 4 : 6) ? 2 : 3);
 };
 
 template <typename T, int D, int NT>
@@ -387,11 +389,11 @@ __global__ void __launch_bounds__(kWarps * 32, (CtaShape<T, D, NT>::kMinCtas))
             sum[nt][1] += w[1] + w[3];
             heaviest = fmaxf(heaviest, fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3])));
             if constexpr (F32) {
-              uint32_t a[3], b[3];
+              uint32_t a[PARTS], b[PARTS];
               split_pair(w[0], w[1], a);
               split_pair(w[2], w[3], b);
 #pragma unroll
-              for (int k = 0; k < 3; ++k)
+              for (int k = 0; k < PARTS; ++k)
                 *reinterpret_cast<uint2 *>(p_at + u * P_BLOCK + (k * NT + nt) * 256) =
                     make_uint2(movm_t(a[k]), movm_t(b[k]));
             } else {
@@ -626,15 +628,17 @@ template <typename T, int D, int NT> bool take(KernelInfo *info, Launch *launch)
   return true;
 }
 
-// Tiles built: 1 to 6 and 8 at head_dim <= 128, 1, 2 and 4 at 256 (float32: 1 to 4,
-// 1 and 2); another number takes the next one.  float32: 32 rows in one pass 95.6
-// us, in two of 16 rows 100.
+// Tiles built: 1 to 6 and 8 at head_dim <= 128, 1, 2 and 4 at 256 (float32: 1 to 6,
+// 1 and 2); another number takes the next one.  float32: 40 rows in one pass 84.5 us,
+// in two 103; 48 rows 70.4 and 73.6.
 template <typename T, int D> bool pick_nt(int nt, KernelInfo *info, Launch *launch) {
   if constexpr (std::is_same<T, float>::value && D <= 128) {
     return nt == 1   ? take<T, D, 1>(info, launch)
            : nt == 2 ? take<T, D, 2>(info, launch)
            : nt == 3 ? take<T, D, 3>(info, launch)
            : nt == 4 ? take<T, D, 4>(info, launch)
+           : nt == 5 ? take<T, D, 5>(info, launch)
+           : nt == 6 ? take<T, D, 6>(info, launch)
                      : false;
   } else if constexpr (std::is_same<T, float>::value) {
     return nt == 1 ? take<T, D, 1>(info, launch) : nt == 2 && take<T, D, 2>(info, launch);
@@ -680,8 +684,8 @@ bool pick(pkv_dtype q_dtype, int D, int nt, KernelInfo *info, Launch *launch) {
 }  // namespace fp4
 
 int cta_fp4_max_tiles(pkv_dtype q_dtype, int head_dim) {
-  const int most = q_dtype == PKV_F32 ? 4 : 8;
-  return head_dim <= 128 ? most : most / 2;
+  const int most = q_dtype == PKV_F32 ? 6 : 8;
+  return head_dim <= 128 ? most : q_dtype == PKV_F32 ? 2 : 4;
 }
 
 bool cta_fp4_kernel_info(pkv_dtype q_dtype, int head_dim, int tiles, KernelInfo *info) {

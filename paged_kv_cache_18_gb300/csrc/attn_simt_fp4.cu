@@ -13,7 +13,7 @@
 // Rows past the context are left out of both, so what they hold never matters.
 // Its sums are the plain float32 ones of the formulas, and it is what kernel =
 // PKV_KERNEL_SIMT asks for: the tensor-core kernels serve every type faster (float32
-// GQA decode, 64 contexts of up to 4352 rows, 267 us here and 78 there).  Bound by
+// GQA decode, 64 contexts of up to 4352 rows, 267 us here and 69 there).  Bound by
 // the issue of its FMAs and shuffles, 450 instructions a block with one row and
 // about 1100 with four.
 #include "fp4.cuh"
