@@ -99,7 +99,8 @@ def run(wl, kernel=0, split_blocks=0, k_scale=K_SCALE, v_scale=V_SCALE, q_gain=N
     got = host_f64(out if wl.num_queries > 1 else out[:, None], wl.dtype)
     check(got, ref, tol, wl.name)
     if keep is not None:
-        keep.update(b=b, dk=dk, dv=dv, q=q, out=out)
+        keep.update(b=b, dk=dk, dv=dv, q=q, out=out, table=torch.from_numpy(b.block_table).to(DEV),
+                    lens=torch.from_numpy(b.context_lens).to(DEV))
     return got, ref
 
 
@@ -517,6 +518,65 @@ def test_side_stream_given_output_and_dirty_workspace():
     assert torch.equal(out, keep["out"])
     with pytest.raises(pkv.PkvError):
         keep["call"](workspace=ws[: need - 16])
+
+
+def test_two_streams_at_once():
+    # calls that run side by side, a workspace each, give what they give alone
+    keeps, alone = [], []
+    for i, (dtype, Q) in enumerate([("bf16", 1), ("f32", 3)]):
+        keep = {}
+        run(W.Workload("fp4 streams", 6, 16, 4, 128, dtype, context_lens=[Q, 900, 2500, 33, 1600, 16],
+                       num_queries=Q, seed=2230 + i), keep=keep)
+        keeps.append((keep, torch.cuda.Stream()))
+        alone.append(keep["out"].clone())
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = []
+        for keep, stream in keeps:
+            b = keep["b"]
+            with torch.cuda.stream(stream):
+                got.append(pkv.paged_attention_fp4(
+                    keep["q"], keep["dk"], keep["dv"], keep["table"], keep["lens"], K_SCALE, V_SCALE,
+                    scale=b.wl.softmax_scale, max_context_len=2500))
+        torch.cuda.synchronize()
+        for g, a in zip(got, alone):
+            assert torch.equal(g, a)
+
+
+@pytest.mark.parametrize("dtype,Q", [("bf16", 1), ("f32", 1), ("f16", 5)])
+def test_more_sequences_than_the_balanced_partition_takes(dtype, Q):
+    lens = [Q + (37 * i) % 300 for i in range(1100)]
+    p = pkv.plan(len(lens), Q, 2, 1, 64, max(lens), "fp4")
+    assert p["stream_k"] == 0
+    run(W.Workload("fp4 many", len(lens), 2, 1, 64, dtype, context_lens=lens, num_queries=Q,
+                   seed=2240 + Q))
+
+
+@pytest.mark.parametrize("kernel", [0, 1])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("L", [100, 2000])
+def test_a_query_that_is_not_finite_is_its_own_affair(dtype, kernel, L):
+    keep = {}
+    run(W.Workload("fp4 not finite", 3, 8, 2, 128, dtype, context_lens=[L, L - 7, 40], seed=2250),
+        kernel=kernel, keep=keep)
+    q = keep["q"].clone()
+    flat = q.view(3, 8, 128)
+    flat[0, 1, 5], flat[1, 6, 127], flat[2, 3, 0] = float("nan"), float("inf"), float("-inf")
+    call = lambda x: pkv.paged_attention_fp4(  # noqa: E731
+        x, keep["dk"], keep["dv"], keep["table"], keep["lens"], K_SCALE, V_SCALE,
+        scale=keep["b"].wl.softmax_scale, max_context_len=L, kernel=kernel)
+    want, got = call(keep["q"]).view(3, 8, 128), call(q).view(3, 8, 128)
+    for b in range(3):
+        for h in range(8):
+            if (b, h) in ((0, 1), (1, 6), (2, 3)):
+                assert torch.isnan(got[b, h]).all()
+            else:
+                assert torch.isfinite(got[b, h]).all()
+                # (another reference may be taken: each is within half a bf16 step of the
+                # output, 2^-8, and the weights' 2^-11 and 2^-13 of the formula's value)
+                far = (got[b, h].float() - want[b, h].float()).abs().max().item()
+                near = 2 * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -13)
+                assert far <= near * want[b].float().abs().max().item()
 
 
 def test_calls_are_bitwise_repeatable():
